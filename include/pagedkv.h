@@ -31,14 +31,15 @@
  *   launched.  A launch failure returns PA_ERR_CUDA (pa_last_cuda_error() gives
  *   the cudaError_t).  The library never aborts the process and never traps on
  *   the device.
- * - Every kernel is launched with programmatic dependent launch and lets the
- *   next kernel of the stream start early.  The decode kernels read seq_lens,
+ * - Every kernel is launched with programmatic dependent launch and, with the
+ *   exceptions below, lets the next kernel of the stream start early.  The decode kernels read seq_lens,
  *   block_tables and query, and the pa_append_decode_kv* kernels seq_lens,
  *   block_tables, cow_src and the new key / value rows, before waiting for the
- *   previous kernel of the stream to finish (everything else after it); no
- *   kernel of this library writes those, and a kernel launched without that
- *   attribute (or one that never triggers its dependents early) is waited for
- *   as usual.
+ *   previous kernel of the stream to finish (everything else after it); the
+ *   kernels of this library that write those (pa_qk_norm_rope*, pa_prepare_batch,
+ *   pa_release_blocks) never let the next kernel start early, and a kernel
+ *   launched without that attribute (or one that never triggers its dependents
+ *   early) is waited for as usual.
  * - Preconditions NOT checked in the launch path (pa_validate_tables checks
  *   them on the device): table entries below num_blocks for the blocks a
  *   sequence uses; ceil(seq_len/block_size) <= max_blocks_per_seq;
@@ -355,6 +356,165 @@ int pa_decode_fp8_split(void *out, const void *query, const void *key_cache,
                         void *stream);
 
 /* --------------------------------------------------------------------------
+ * 4-bit KV cache: half a byte per cached K/V element plus one (scale, zero)
+ * pair per row, 72 % smaller than bf16 at head_dim 128.  A row is the head_dim
+ * values of one token and KV head.
+ *   key_cache, value_cache: uint8 [num_blocks, num_kv_heads, record] with
+ *   record = block_size * (head_dim / 2 + 4) bytes:
+ *     block_size rows of head_dim / 2 bytes, byte i of a row holding the code
+ *     of dim 2i in its low nibble and of dim 2i + 1 in its high nibble, then
+ *     block_size pairs (scale, zero) of bf16.
+ *   A code c stands for zero + scale * c.
+ * A row x (bf16) is quantised as
+ *   zero = min x, scale = bf16(fp32(max x * r) - fp32(min x * r)), r = fp32(1/15),
+ *   code = clamp(rint(fp32(fp32(x - zero) * fp32(1 / scale))), 0, 15),
+ * every step one fp32 operation rounded to nearest even.  Where the scale would
+ * be below 2^-126 it is 0 and so are the codes.  A row that holds a NaN or an
+ * infinity stands for NaN throughout (zero = NaN, scale = 0, codes 0).
+ * Supported: head_dim 64 or 128, block_size 8, 16 or 32.
+ *
+ * pa_reshape_and_cache_int4: pa_reshape_and_cache with quantisation.  key and
+ * value: bf16, token t's num_kv_heads * head_dim values start key_stride /
+ * value_stride elements after token t-1's (a multiple of 8, at least
+ * num_kv_heads * head_dim), so views into a fused projection serve as they are.
+ * Slots: a negative slot, or one at or past num_blocks * block_size, skips the
+ * token; the others must be distinct.
+ * pa_append_decode_kv_int4: the slot rules and outputs of pa_append_decode_kv.
+ * pa_dequantize_blocks_int4: blocks block_ids[0..num_ids) (int32, device) as
+ * bf16 blocks key_out / value_out [num_ids, block_size, num_kv_heads, head_dim]
+ * -- the cache layout of pa_prefill, for a chunk that follows 4-bit context.
+ * value = bf16(fma(scale, code, zero)).  An id outside [0, num_blocks) leaves
+ * its output block as it was; ids may repeat.
+ * ------------------------------------------------------------------------ */
+int pa_reshape_and_cache_int4(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
+                              void *key_cache, void *value_cache, const int64_t *slot_mapping, int num_tokens,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks, void *stream);
+int pa_append_decode_kv_int4(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
+                             void *key_cache, void *value_cache, const int32_t *block_tables,
+                             const int32_t *seq_lens, int64_t *slot_mapping, int num_seqs,
+                             int max_blocks_per_seq, int num_kv_heads, int head_dim, int block_size,
+                             int num_blocks, void *stream);
+int pa_dequantize_blocks_int4(void *key_out, void *value_out, const void *key_cache, const void *value_cache,
+                              const int32_t *block_ids, int num_ids, int num_kv_heads, int head_dim,
+                              int block_size, int num_blocks, void *stream);
+
+/* Single-query paged decode over a 4-bit cache: the result of pa_decode with K
+ * and V the values the codes stand for (G = num_heads / num_kv_heads in 1..16).
+ * The work is split over the GPU by the lengths found on the device, so no
+ * bound of the lengths is passed; one launch.  A length of 0 or less gives
+ * zeros, a length past max_blocks_per_seq * block_size counts as that.  A table
+ * entry outside [0, num_blocks) among the blocks of a sequence is not followed:
+ * the sequence's outputs are NaN for the KV heads concerned (all of them) and
+ * pa_device_status reports PA_ERR_BAD_BLOCK.  A row that stands for NaN makes
+ * the outputs of its sequence and KV head NaN.
+ * workspace: pa_decode_int4_workspace_size bytes (which does not depend on the
+ * batch), 16-byte aligned, ZERO-FILLED ONCE after allocation; each call leaves
+ * it ready for the next.  Calls that may run at the same time (two streams, two
+ * captured graphs) must not share one.  num_seqs <= 65535. */
+size_t pa_decode_int4_workspace_size(int num_heads, int num_kv_heads, int head_dim);
+int pa_decode_int4(void *out, const void *query, const void *key_cache, const void *value_cache,
+                   const int32_t *block_tables, const int32_t *seq_lens, float scale, int block_size,
+                   int num_kv_heads, int num_seqs, int num_heads, int head_dim, int max_blocks_per_seq,
+                   int num_blocks, void *workspace, size_t workspace_bytes, void *stream);
+
+/* --------------------------------------------------------------------------
+ * RMS norm of every query and key head with the position rotation, in one pass
+ * over what the projection left, and (the _cache forms) the write of K and V
+ * into the cache:
+ *   y = x / sqrt(mean(x^2) + eps) * weight         (over the head's head_dim)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)       for each of rot_dim/2 pairs
+ * with pairs (i, i + rot_dim/2), or (2i, 2i + 1) where interleaved != 0; dims
+ * from rot_dim on are only normed.  fp32 throughout, rounded to bf16 once.
+ *   query, key, value: bf16 rows with token strides (elements, multiples of 8),
+ *   e.g. views into one fused projection; query_out, key_out: the same, and may
+ *   be the inputs themselves (same pointer and stride), not overlap otherwise;
+ *   q_weight, k_weight: bf16 [head_dim], NULL = ones;
+ *   cos_sin: fp32 [max_position, rot_dim], a row holding rot_dim/2 cosines and
+ *   then rot_dim/2 sines; positions: int64 [num_tokens].
+ * A token whose position is outside [0, max_position) is padding: nothing of it
+ * is written.  A token whose slot is negative or past the cache has its queries
+ * written but no cache row.  Sums of squares are fp32: a head with entries above
+ * about 1e18 overflows them.  head_dim 64 or 128; rot_dim a multiple of 16 up to
+ * head_dim; eps >= 0 and finite.
+ *   pa_qk_norm_rope             query_out, key_out; no cache;
+ *   pa_qk_norm_rope_cache       caches of pa_reshape_and_cache (bf16);
+ *   pa_qk_norm_rope_cache_fp8   caches of pa_reshape_and_cache_fp8;
+ *   pa_qk_norm_rope_cache_int4  caches of pa_reshape_and_cache_int4.
+ * The cached keys are the rounded bf16 results (quantised from those in the
+ * last two), so each form equals pa_qk_norm_rope followed by the cache write.
+ * These kernels write queries, which later kernels may read before waiting:
+ * they never let the next kernel start early.
+ * ------------------------------------------------------------------------ */
+int pa_qk_norm_rope(void *query_out, void *key_out, const void *query, const void *key, const void *q_weight,
+                    const void *k_weight, const float *cos_sin, const int64_t *positions, float eps,
+                    int64_t query_out_stride, int64_t key_out_stride, int64_t query_stride, int64_t key_stride,
+                    int rot_dim, int interleaved, int max_position, int num_tokens, int num_heads,
+                    int num_kv_heads, int head_dim, void *stream);
+int pa_qk_norm_rope_cache(void *query_out, const void *query, const void *key, const void *value,
+                          const void *q_weight, const void *k_weight, const float *cos_sin,
+                          const int64_t *positions, const int64_t *slot_mapping, void *key_cache,
+                          void *value_cache, float eps, int64_t query_out_stride, int64_t query_stride,
+                          int64_t key_stride, int64_t value_stride, int rot_dim, int interleaved,
+                          int max_position, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                          int block_size, int num_blocks, void *stream);
+int pa_qk_norm_rope_cache_fp8(void *query_out, const void *query, const void *key, const void *value,
+                              const void *q_weight, const void *k_weight, const float *cos_sin,
+                              const int64_t *positions, const int64_t *slot_mapping, void *key_cache,
+                              void *value_cache, float eps, int64_t query_out_stride, int64_t query_stride,
+                              int64_t key_stride, int64_t value_stride, int rot_dim, int interleaved,
+                              int max_position, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                              int block_size, int num_blocks, float k_scale, float v_scale, void *stream);
+int pa_qk_norm_rope_cache_int4(void *query_out, const void *query, const void *key, const void *value,
+                               const void *q_weight, const void *k_weight, const float *cos_sin,
+                               const int64_t *positions, const int64_t *slot_mapping, void *key_cache,
+                               void *value_cache, float eps, int64_t query_out_stride, int64_t query_stride,
+                               int64_t key_stride, int64_t value_stride, int rot_dim, int interleaved,
+                               int max_position, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                               int block_size, int num_blocks, void *stream);
+
+/* --------------------------------------------------------------------------
+ * A step's block tables, lengths and slots built on the device from the
+ * requests' lengths: the counterpart of pa_pool_prepare_decode for batches
+ * whose lengths never leave the GPU (prompt chunks and decodes mixed).  The free
+ * blocks are a stack in device memory, handed out from its end; blocks have one
+ * owner (sharing and copy-on-write stay with the host pool).
+ *   context_lens, query_lens: int32 [num_seqs], cached and new tokens;
+ *   free_blocks: int32 [free_capacity]; num_free: int32 [1], how many are free.
+ * With have = ceil(context / block_size), need = ceil((context + new) /
+ * block_size) - have and before_s = the needs of the requests before s:
+ *   block_tables[s][have + j] = free_blocks[num_free - 1 - before_s - j], j < need;
+ *   seq_lens[s] = context + new;  q_start: int32 [num_seqs + 1], sums of new;
+ *   row t < q_start[num_seqs]: seq_ids[t] = s (int32), positions[t] (int64),
+ *   slot_mapping[t] (int64, from the table); rows up to num_tokens hold -1;
+ *   num_free_out: int32 [1] (may be num_free itself);
+ *   status: int32 [1], PA_OK, PA_ERR_POOL_EXHAUSTED (the needs exceed num_free),
+ *   PA_ERR_BAD_SHAPE (a negative length, one past the table row, more than
+ *   num_tokens new tokens, num_free outside [0, free_capacity]) or
+ *   PA_ERR_BAD_BLOCK (a free block handed out is outside [0, num_blocks); its
+ *   table entry and slots are -1).
+ * With one of the first two errors nothing is handed out: the tables stay as
+ * they are, seq_lens are the context lengths (clamped to the row), q_start is 0
+ * and every row -1.  seq_ids, positions and slot_mapping may be NULL; seq_lens
+ * may be context_lens itself.
+ * The seq_lens and tables written here may be read by later kernels before they
+ * wait: these kernels never let the next kernel start early.
+ *
+ * pa_release_blocks: the blocks of every request with release[s] != 0 (int32)
+ * go back on the stack, in request order and each row's blocks in order; the
+ * row's entries become -1 and seq_lens[s] 0.  status: PA_OK, PA_ERR_BAD_SHAPE
+ * (a length outside the row, or the stack would overflow) or PA_ERR_BAD_BLOCK
+ * (an entry outside the cache); with an error nothing changes.
+ * ------------------------------------------------------------------------ */
+int pa_prepare_batch(int32_t *block_tables, const int32_t *context_lens, const int32_t *query_lens,
+                     const int32_t *free_blocks, const int32_t *num_free, int32_t *seq_lens, int32_t *q_start,
+                     int32_t *seq_ids, int64_t *positions, int64_t *slot_mapping, int32_t *num_free_out,
+                     int32_t *status, int num_seqs, int max_blocks_per_seq, int num_tokens, int free_capacity,
+                     int block_size, int num_blocks, void *stream);
+int pa_release_blocks(int32_t *block_tables, int32_t *seq_lens, const int32_t *release, int32_t *free_blocks,
+                      int32_t *num_free, int32_t *status, int num_seqs, int max_blocks_per_seq,
+                      int free_capacity, int block_size, int num_blocks, void *stream);
+
+/* --------------------------------------------------------------------------
  * Multi-query paged prefill: the chunked-prefill step ([深度解析], milestone
  * list: v0.5 "Chunked Prefill" -- a long prompt is fed in chunks so that it
  * does not hold up decodes) with the causal rule of [论文专题] (the query at
@@ -439,8 +599,9 @@ int pa_decode_split_noalloc(void *out, const void *query, const void *key_cache,
  * nonzero code in a device word and lets the kernel return.  This call reads
  * and clears that word for the current device (synchronising the device);
  * 0 means no wait ever gave up and no kernel met an out-of-range value;
- * otherwise PA_ERR_DEVICE_TIMEOUT, or PA_ERR_VALUE_RANGE when pa_prefill read
- * a value-cache entry of magnitude above 65504 (its P.V operand is fp16). */
+ * otherwise PA_ERR_DEVICE_TIMEOUT, PA_ERR_VALUE_RANGE when pa_prefill read
+ * a value-cache entry of magnitude above 65504 (its P.V operand is fp16), or
+ * PA_ERR_BAD_BLOCK when pa_decode_int4 met a table entry outside the cache. */
 int pa_device_status(void);
 
 /* Self-test of the bounded-wait path: launches one thread that waits on an

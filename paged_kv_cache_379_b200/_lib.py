@@ -17,6 +17,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
+_L = ctypes.c_int64
 
 # name -> (restype, argtypes), mirroring include/pagedkv.h
 SIGNATURES = {
@@ -33,6 +34,17 @@ SIGNATURES = {
     "pa_append_decode_kv": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "pa_append_decode_kv_cow": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "pa_append_decode_kv_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _F, _P]),
+    "pa_reshape_and_cache_int4": (_I, [_P, _P, _L, _L, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "pa_append_decode_kv_int4": (_I, [_P, _P, _L, _L, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "pa_dequantize_blocks_int4": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "pa_decode_int4_workspace_size": (_SZ, [_I, _I, _I]),
+    "pa_decode_int4": (_I, [_P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _I, _I, _I, _P, _SZ, _P]),
+    "pa_qk_norm_rope": (_I, [_P] * 8 + [_F, _L, _L, _L, _L] + [_I] * 7 + [_P]),
+    "pa_qk_norm_rope_cache": (_I, [_P] * 11 + [_F, _L, _L, _L, _L] + [_I] * 9 + [_P]),
+    "pa_qk_norm_rope_cache_fp8": (_I, [_P] * 11 + [_F, _L, _L, _L, _L] + [_I] * 9 + [_F, _F, _P]),
+    "pa_qk_norm_rope_cache_int4": (_I, [_P] * 11 + [_F, _L, _L, _L, _L] + [_I] * 9 + [_P]),
+    "pa_prepare_batch": (_I, [_P] * 12 + [_I] * 6 + [_P]),
+    "pa_release_blocks": (_I, [_P] * 6 + [_I] * 5 + [_P]),
     "pa_copy_blocks": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "pa_swap_blocks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "pa_decode": (_I, [_P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _I, _I, _I, _I, _P, _SZ, _P]),

@@ -28,6 +28,9 @@ constexpr int kTimeoutDrain = 3;
 // Code written when a kernel met an input value outside the range of the
 // arithmetic it uses (the prefill's fp16 P.V operand: |v| > 65504).
 constexpr int kStatusValueRange = 4;
+// Code written when the 4-bit decode met a block-table entry outside the cache
+// (the block is not read).
+constexpr int kStatusBadBlock = 5;
 // A wait gives up after this many nanoseconds of %globaltimer.
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 

@@ -1,6 +1,7 @@
 // pagedkv.cu -- the C ABI of libpagedkv.so (declared in include/pagedkv.h):
 // argument checks, TMA tensor-map encoding, kernel selection and launch.
-// The kernels themselves are in cache_ops.cuh and decode.cuh.
+// The kernels themselves are in cache_ops.cuh, decode.cuh, prefill.cuh, row_ops.cuh,
+// decode_int4.cuh and batch_ops.cuh.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -8,10 +9,13 @@
 #include <tuple>
 #include <vector>
 
+#include "batch_ops.cuh"
 #include "cache_ops.cuh"
 #include "common.cuh"
 #include "decode.cuh"
+#include "decode_int4.cuh"
 #include "prefill.cuh"
+#include "row_ops.cuh"
 
 namespace pakv {
 
@@ -399,6 +403,158 @@ __global__ void bounded_wait_selftest_kernel()
     mbar_init(b, 1);
     fence_mbarrier_init();
     if (!mbar_wait_bounded(b, 0)) record_timeout(kTimeoutFullBarrier);
+}
+
+// ------------------------------------------- head norm + rotation, 4-bit cache write
+
+// Token strides (elements) and alignment of a [T, heads, D] view whose last two
+// dimensions are contiguous.
+static int check_rows(const void *ptr, int64_t stride, int heads, int d, int num_tokens)
+{
+    if (!ptr) return PA_ERR_NULL_POINTER;
+    if (num_tokens > 1 && stride < (int64_t)heads * d) return PA_ERR_BAD_SHAPE;
+    if (!aligned16(ptr) || stride % 8 != 0) return PA_ERR_ALIGNMENT;
+    return PA_OK;
+}
+
+static int check_int4_cache(const void *key_cache, const void *value_cache, int num_kv_heads, int head_dim,
+                            int block_size, int num_blocks)
+{
+    if (num_kv_heads <= 0 || num_blocks <= 0) return PA_ERR_BAD_SHAPE;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)num_blocks * block_size > INT_MAX) return PA_ERR_BAD_SHAPE;
+    if (!key_cache || !value_cache) return PA_ERR_NULL_POINTER;
+    if (!aligned16(key_cache) || !aligned16(value_cache)) return PA_ERR_ALIGNMENT;
+    return PA_OK;
+}
+
+template <int CACHE, bool ROPE>
+static int launch_rows(RowParams &p, int head_dim, int num_tokens, bool interleaved, cudaStream_t st)
+{
+    const int per_warp = 4 * (32 / (head_dim / 8));  // rows one warp takes
+    p.chunks = (p.rows + per_warp - 1) / per_warp;
+    const int64_t units = (int64_t)num_tokens * p.chunks;
+    if (units > INT_MAX - 8) return PA_ERR_BAD_SHAPE;
+    p.units = (int)units;
+    const dim3 grid((unsigned)((units + 7) / 8)), block(256);
+    if constexpr (ROPE) {
+        if (interleaved)
+            return head_dim == 64 ? launch_pdl(row_kernel<64, CACHE, true, true>, grid, block, 0, st, p)
+                                  : launch_pdl(row_kernel<128, CACHE, true, true>, grid, block, 0, st, p);
+        return head_dim == 64 ? launch_pdl(row_kernel<64, CACHE, true, false>, grid, block, 0, st, p)
+                              : launch_pdl(row_kernel<128, CACHE, true, false>, grid, block, 0, st, p);
+    } else {
+        return head_dim == 64 ? launch_pdl(row_kernel<64, CACHE, false, false>, grid, block, 0, st, p)
+                              : launch_pdl(row_kernel<128, CACHE, false, false>, grid, block, 0, st, p);
+    }
+}
+
+// K and V rows into a 4-bit cache; the slots come from `slots`, or from the
+// tables and lengths (decode form).
+static int write_int4(const void *key, const void *value, int64_t key_stride, int64_t value_stride, void *key_cache,
+                      void *value_cache, const int64_t *slots, const int32_t *block_tables, const int32_t *seq_lens,
+                      int64_t *slots_out, int num_tokens, int max_blocks, int num_kv_heads, int head_dim,
+                      int block_size, int num_blocks, void *stream)
+{
+    if (num_tokens < 0) return PA_ERR_BAD_SHAPE;
+    int rc = check_int4_cache(key_cache, value_cache, num_kv_heads, head_dim, block_size, num_blocks);
+    if (rc != PA_OK && !(rc == PA_ERR_NULL_POINTER && num_tokens == 0)) return rc;
+    if (num_tokens == 0) return PA_OK;
+    rc = check_rows(key, key_stride, num_kv_heads, head_dim, num_tokens);
+    if (rc == PA_OK) rc = check_rows(value, value_stride, num_kv_heads, head_dim, num_tokens);
+    if (rc != PA_OK) return rc;
+    RowParams p = {};
+    p.key = static_cast<const __nv_bfloat16 *>(key);
+    p.value = static_cast<const __nv_bfloat16 *>(value);
+    p.k_stride = key_stride;
+    p.v_stride = value_stride;
+    p.slots = slots;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.slots_out = slots_out;
+    p.max_blocks = max_blocks;
+    p.key_cache = key_cache;
+    p.value_cache = value_cache;
+    p.num_kv_heads = num_kv_heads;
+    p.rows = 2 * num_kv_heads;
+    p.block_size = block_size;
+    p.num_slots = (int64_t)num_blocks * block_size;
+    return launch_rows<kCacheInt4, false>(p, head_dim, num_tokens, false, static_cast<cudaStream_t>(stream));
+}
+
+// The arguments the four pa_qk_norm_rope* entry points share.
+static int rope_params(RowParams &p, void *query_out, const void *query, const void *key, const void *q_weight,
+                       const void *k_weight, const float *cos_sin, const int64_t *positions, float eps,
+                       int64_t qo_stride, int64_t q_stride, int64_t k_stride, int rot_dim, int max_position,
+                       int num_tokens, int num_heads, int num_kv_heads, int head_dim)
+{
+    if (num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || max_position <= 0 || !(eps >= 0.f && eps < INFINITY))
+        return PA_ERR_BAD_SHAPE;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (rot_dim < 16 || rot_dim > head_dim || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PA_OK;
+    int rc = check_rows(query, q_stride, num_heads, head_dim, num_tokens);
+    if (rc == PA_OK) rc = check_rows(key, k_stride, num_kv_heads, head_dim, num_tokens);
+    if (rc == PA_OK) rc = check_rows(query_out, qo_stride, num_heads, head_dim, num_tokens);
+    if (rc != PA_OK) return rc;
+    if (!cos_sin || !positions) return PA_ERR_NULL_POINTER;
+    if (!aligned16(cos_sin) || !aligned16(q_weight) || !aligned16(k_weight)) return PA_ERR_ALIGNMENT;
+    p.query = static_cast<const __nv_bfloat16 *>(query);
+    p.key = static_cast<const __nv_bfloat16 *>(key);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.query_out = static_cast<__nv_bfloat16 *>(query_out);
+    p.qo_stride = qo_stride;
+    p.q_weight = static_cast<const __nv_bfloat16 *>(q_weight);
+    p.k_weight = static_cast<const __nv_bfloat16 *>(k_weight);
+    p.eps = eps;
+    p.cos_sin = cos_sin;
+    p.rot = rot_dim;
+    p.max_position = max_position;
+    p.positions = positions;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.rows = num_heads + num_kv_heads;
+    return PA_OK;
+}
+
+template <int CACHE>
+static int qk_norm_rope_cache(void *query_out, const void *query, const void *key, const void *value,
+                              const void *q_weight, const void *k_weight, const float *cos_sin,
+                              const int64_t *positions, const int64_t *slot_mapping, void *key_cache,
+                              void *value_cache, float eps, int64_t qo_stride, int64_t q_stride, int64_t k_stride,
+                              int64_t v_stride, int rot_dim, int interleaved, int max_position, int num_tokens,
+                              int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                              float k_scale, float v_scale, void *stream)
+{
+    RowParams p = {};
+    int rc = rope_params(p, query_out, query, key, q_weight, k_weight, cos_sin, positions, eps, qo_stride, q_stride,
+                         k_stride, rot_dim, max_position, num_tokens, num_heads, num_kv_heads, head_dim);
+    if (rc != PA_OK) return rc;
+    if (block_size <= 0 || num_blocks <= 0) return PA_ERR_BAD_SHAPE;
+    if (CACHE == kCacheFp8 && !(k_scale > 0.f && v_scale > 0.f && k_scale < INFINITY && v_scale < INFINITY))
+        return PA_ERR_BAD_SHAPE;
+    if (CACHE == kCacheInt4) {
+        rc = check_int4_cache(key_cache, value_cache, num_kv_heads, head_dim, block_size, num_blocks);
+        if (rc != PA_OK && !(rc == PA_ERR_NULL_POINTER && num_tokens == 0)) return rc;
+    }
+    if (num_tokens == 0) return PA_OK;
+    if (!key_cache || !value_cache || !slot_mapping) return PA_ERR_NULL_POINTER;
+    if (!aligned16(key_cache) || !aligned16(value_cache)) return PA_ERR_ALIGNMENT;
+    rc = check_rows(value, v_stride, num_kv_heads, head_dim, num_tokens);
+    if (rc != PA_OK) return rc;
+    p.value = static_cast<const __nv_bfloat16 *>(value);
+    p.v_stride = v_stride;
+    p.slots = slot_mapping;
+    p.key_cache = key_cache;
+    p.value_cache = value_cache;
+    p.rows += num_kv_heads;
+    p.block_size = block_size;
+    p.num_slots = (int64_t)num_blocks * block_size;
+    p.k_inv = 1.0f / k_scale;  // rounded to fp32 once, as the FP8 cache write does
+    p.v_inv = 1.0f / v_scale;
+    return launch_rows<CACHE, true>(p, head_dim, num_tokens, interleaved != 0, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace pakv
@@ -937,6 +1093,210 @@ int pa_validate_tables(const int32_t *block_tables, const int32_t *seq_lens, int
                       num_seqs, max_blocks_per_seq, block_size, num_blocks, max_seq_len, bad_count);
 }
 
+// ------------------------------------------- head norm + rotation, 4-bit cache write
+
+int pa_reshape_and_cache_int4(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
+                              void *key_cache, void *value_cache, const int64_t *slot_mapping, int num_tokens,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks, void *stream)
+{
+    if (num_tokens > 0 && !slot_mapping) return PA_ERR_NULL_POINTER;
+    return write_int4(key, value, key_stride, value_stride, key_cache, value_cache, slot_mapping, nullptr, nullptr,
+                      nullptr, num_tokens, 0, num_kv_heads, head_dim, block_size, num_blocks, stream);
+}
+
+int pa_append_decode_kv_int4(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
+                             void *key_cache, void *value_cache, const int32_t *block_tables, const int32_t *seq_lens,
+                             int64_t *slot_mapping, int num_seqs, int max_blocks_per_seq, int num_kv_heads,
+                             int head_dim, int block_size, int num_blocks, void *stream)
+{
+    if (max_blocks_per_seq <= 0) return PA_ERR_BAD_SHAPE;
+    if (num_seqs > 0 && (!block_tables || !seq_lens)) return PA_ERR_NULL_POINTER;
+    return write_int4(key, value, key_stride, value_stride, key_cache, value_cache, nullptr, block_tables, seq_lens,
+                      slot_mapping, num_seqs, max_blocks_per_seq, num_kv_heads, head_dim, block_size, num_blocks,
+                      stream);
+}
+
+int pa_dequantize_blocks_int4(void *key_out, void *value_out, const void *key_cache, const void *value_cache,
+                              const int32_t *block_ids, int num_ids, int num_kv_heads, int head_dim, int block_size,
+                              int num_blocks, void *stream)
+{
+    if (num_ids < 0) return PA_ERR_BAD_SHAPE;
+    const int rc = check_int4_cache(key_cache, value_cache, num_kv_heads, head_dim, block_size, num_blocks);
+    if (rc != PA_OK && !(rc == PA_ERR_NULL_POINTER && num_ids == 0)) return rc;
+    if (num_ids == 0) return PA_OK;
+    if (!key_out || !value_out || !block_ids) return PA_ERR_NULL_POINTER;
+    if (!aligned16(key_out) || !aligned16(value_out)) return PA_ERR_ALIGNMENT;
+    const int64_t units = (int64_t)num_ids * num_kv_heads * 2;
+    if (cdiv64(units, 8) > INT_MAX) return PA_ERR_BAD_SHAPE;
+    return launch_pdl(head_dim == 64 ? dequantize_blocks_int4_kernel<64> : dequantize_blocks_int4_kernel<128>,
+                      dim3((unsigned)cdiv64(units, 8)), dim3(256), 0, static_cast<cudaStream_t>(stream),
+                      static_cast<__nv_bfloat16 *>(key_out), static_cast<__nv_bfloat16 *>(value_out),
+                      static_cast<const uint8_t *>(key_cache), static_cast<const uint8_t *>(value_cache), block_ids,
+                      units, num_kv_heads, block_size, num_blocks);
+}
+
+int pa_qk_norm_rope(void *query_out, void *key_out, const void *query, const void *key, const void *q_weight,
+                    const void *k_weight, const float *cos_sin, const int64_t *positions, float eps,
+                    int64_t query_out_stride, int64_t key_out_stride, int64_t query_stride, int64_t key_stride,
+                    int rot_dim, int interleaved, int max_position, int num_tokens, int num_heads, int num_kv_heads,
+                    int head_dim, void *stream)
+{
+    RowParams p = {};
+    int rc = rope_params(p, query_out, query, key, q_weight, k_weight, cos_sin, positions, eps, query_out_stride,
+                         query_stride, key_stride, rot_dim, max_position, num_tokens, num_heads, num_kv_heads,
+                         head_dim);
+    if (rc != PA_OK || num_tokens == 0) return rc;
+    rc = check_rows(key_out, key_out_stride, num_kv_heads, head_dim, num_tokens);
+    if (rc != PA_OK) return rc;
+    p.key_out = static_cast<__nv_bfloat16 *>(key_out);
+    p.ko_stride = key_out_stride;
+    return launch_rows<kCacheNone, true>(p, head_dim, num_tokens, interleaved != 0, static_cast<cudaStream_t>(stream));
+}
+
+int pa_qk_norm_rope_cache(void *query_out, const void *query, const void *key, const void *value,
+                          const void *q_weight, const void *k_weight, const float *cos_sin, const int64_t *positions,
+                          const int64_t *slot_mapping, void *key_cache, void *value_cache, float eps,
+                          int64_t query_out_stride, int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                          int rot_dim, int interleaved, int max_position, int num_tokens, int num_heads,
+                          int num_kv_heads, int head_dim, int block_size, int num_blocks, void *stream)
+{
+    return qk_norm_rope_cache<kCacheBf16>(query_out, query, key, value, q_weight, k_weight, cos_sin, positions,
+                                          slot_mapping, key_cache, value_cache, eps, query_out_stride, query_stride,
+                                          key_stride, value_stride, rot_dim, interleaved, max_position, num_tokens,
+                                          num_heads, num_kv_heads, head_dim, block_size, num_blocks, 1.f, 1.f, stream);
+}
+
+int pa_qk_norm_rope_cache_fp8(void *query_out, const void *query, const void *key, const void *value,
+                              const void *q_weight, const void *k_weight, const float *cos_sin,
+                              const int64_t *positions, const int64_t *slot_mapping, void *key_cache,
+                              void *value_cache, float eps, int64_t query_out_stride, int64_t query_stride,
+                              int64_t key_stride, int64_t value_stride, int rot_dim, int interleaved,
+                              int max_position, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                              int block_size, int num_blocks, float k_scale, float v_scale, void *stream)
+{
+    return qk_norm_rope_cache<kCacheFp8>(query_out, query, key, value, q_weight, k_weight, cos_sin, positions,
+                                         slot_mapping, key_cache, value_cache, eps, query_out_stride, query_stride,
+                                         key_stride, value_stride, rot_dim, interleaved, max_position, num_tokens,
+                                         num_heads, num_kv_heads, head_dim, block_size, num_blocks, k_scale, v_scale,
+                                         stream);
+}
+
+int pa_qk_norm_rope_cache_int4(void *query_out, const void *query, const void *key, const void *value,
+                               const void *q_weight, const void *k_weight, const float *cos_sin,
+                               const int64_t *positions, const int64_t *slot_mapping, void *key_cache,
+                               void *value_cache, float eps, int64_t query_out_stride, int64_t query_stride,
+                               int64_t key_stride, int64_t value_stride, int rot_dim, int interleaved,
+                               int max_position, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                               int block_size, int num_blocks, void *stream)
+{
+    return qk_norm_rope_cache<kCacheInt4>(query_out, query, key, value, q_weight, k_weight, cos_sin, positions,
+                                          slot_mapping, key_cache, value_cache, eps, query_out_stride, query_stride,
+                                          key_stride, value_stride, rot_dim, interleaved, max_position, num_tokens,
+                                          num_heads, num_kv_heads, head_dim, block_size, num_blocks, 1.f, 1.f, stream);
+}
+
+// ------------------------------------------------------------- 4-bit cache decode
+
+size_t pa_decode_int4_workspace_size(int num_heads, int num_kv_heads, int head_dim)
+{
+    if (num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_heads % num_kv_heads != 0) return 0;
+    return kSchedBytes;
+}
+
+int pa_decode_int4(void *out, const void *query, const void *key_cache, const void *value_cache,
+                   const int32_t *block_tables, const int32_t *seq_lens, float scale, int block_size,
+                   int num_kv_heads, int num_seqs, int num_heads, int head_dim, int max_blocks_per_seq,
+                   int num_blocks, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0) return PA_ERR_BAD_SHAPE;
+    if (num_heads % num_kv_heads != 0) return PA_ERR_BAD_SHAPE;
+    if (num_heads / num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
+    const int rc = check_int4_cache(key_cache, value_cache, num_kv_heads, head_dim, block_size, num_blocks);
+    if (rc != PA_OK) return rc;
+    if ((int64_t)max_blocks_per_seq * block_size > INT_MAX) return PA_ERR_BAD_SHAPE;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !query || !block_tables || !seq_lens) return PA_ERR_NULL_POINTER;
+    if (!aligned16(out) || !aligned16(query)) return PA_ERR_ALIGNMENT;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < pa_decode_int4_workspace_size(num_heads, num_kv_heads, head_dim))
+        return PA_ERR_WORKSPACE;
+    if (num_seqs > 65535) return PA_ERR_BAD_SHAPE;
+    Int4DecodeParams p = {};
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.query = static_cast<const __nv_bfloat16 *>(query);
+    p.key_cache = static_cast<const uint8_t *>(key_cache);
+    p.value_cache = static_cast<const uint8_t *>(value_cache);
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.workspace = workspace;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.num_seqs = num_seqs;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_heads / num_kv_heads;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    return launch_pdl(head_dim == 64 ? decode_int4_simple_kernel<64> : decode_int4_simple_kernel<128>,
+                      dim3((unsigned)num_kv_heads, (unsigned)num_seqs), dim3(128), 0,
+                      static_cast<cudaStream_t>(stream), p, block_size);
+}
+
+// ----------------------------------------------------------- a step's tables and slots
+
+int pa_prepare_batch(int32_t *block_tables, const int32_t *context_lens, const int32_t *query_lens,
+                     const int32_t *free_blocks, const int32_t *num_free, int32_t *seq_lens, int32_t *q_start,
+                     int32_t *seq_ids, int64_t *positions, int64_t *slot_mapping, int32_t *num_free_out,
+                     int32_t *status, int num_seqs, int max_blocks_per_seq, int num_tokens, int free_capacity,
+                     int block_size, int num_blocks, void *stream)
+{
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || num_tokens < 0 || free_capacity < 0 || block_size <= 0 ||
+        num_blocks <= 0)
+        return PA_ERR_BAD_SHAPE;
+    if ((int64_t)max_blocks_per_seq * block_size > INT_MAX) return PA_ERR_BAD_SHAPE;
+    if (!num_free || !num_free_out || !status || !q_start) return PA_ERR_NULL_POINTER;
+    if (num_seqs > 0 && (!block_tables || !context_lens || !query_lens || !seq_lens)) return PA_ERR_NULL_POINTER;
+    if (free_capacity > 0 && !free_blocks) return PA_ERR_NULL_POINTER;
+    BatchParams p = {};
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_lens = query_lens;
+    p.free_blocks = free_blocks;
+    p.num_free = num_free;
+    p.seq_lens = seq_lens;
+    p.q_start = q_start;
+    p.seq_ids = seq_ids;
+    p.positions = positions;
+    p.slots = slot_mapping;
+    p.num_free_out = num_free_out;
+    p.status = status;
+    p.num_seqs = num_seqs;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_tokens = num_tokens;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    p.free_capacity = free_capacity;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool fused = num_tokens <= kBatchFusedTokens;
+    const int rc = launch_pdl(prepare_batch_kernel, dim3(1), dim3(kBatchThreads), 0, st, p, fused ? 1 : 0);
+    if (rc != PA_OK || fused) return rc;
+    return launch_pdl(fill_tokens_kernel, dim3((unsigned)cdiv64(num_tokens, 1024)), dim3(256), 0, st, p);
+}
+
+int pa_release_blocks(int32_t *block_tables, int32_t *seq_lens, const int32_t *release, int32_t *free_blocks,
+                      int32_t *num_free, int32_t *status, int num_seqs, int max_blocks_per_seq, int free_capacity,
+                      int block_size, int num_blocks, void *stream)
+{
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || free_capacity < 0 || block_size <= 0 || num_blocks <= 0)
+        return PA_ERR_BAD_SHAPE;
+    if ((int64_t)max_blocks_per_seq * block_size > INT_MAX) return PA_ERR_BAD_SHAPE;
+    if (!num_free || !status) return PA_ERR_NULL_POINTER;
+    if (num_seqs > 0 && (!block_tables || !seq_lens || !release)) return PA_ERR_NULL_POINTER;
+    if (free_capacity > 0 && !free_blocks) return PA_ERR_NULL_POINTER;
+    return launch_pdl(release_blocks_kernel, dim3(1), dim3(kBatchThreads), 0, static_cast<cudaStream_t>(stream),
+                      block_tables, num_seqs, max_blocks_per_seq, seq_lens, release, free_blocks, num_free,
+                      free_capacity, block_size, num_blocks, status);
+}
+
 int pa_device_status(void)
 {
     int rc = check_cuda(cudaDeviceSynchronize());
@@ -948,6 +1308,7 @@ int pa_device_status(void)
         const int zero = 0;
         rc = check_cuda(cudaMemcpyToSymbol(g_pa_device_status, &zero, sizeof(int)));
         if (rc != PA_OK) return rc;
+        if (v == pakv::kStatusBadBlock) return PA_ERR_BAD_BLOCK;
         return v == pakv::kStatusValueRange ? PA_ERR_VALUE_RANGE : PA_ERR_DEVICE_TIMEOUT;
     }
     return PA_OK;

@@ -14,6 +14,8 @@ Tensor conventions (see include/pagedkv.h):
   src_dst_pairs          : int64 [num_pairs, 2]
   FP8 caches             : uint8 E4M3 codes [num_blocks, block_size, num_kv_heads, head_dim]
                            with one fp32 scale per cache (k_scale, v_scale)
+  4-bit caches             : uint8 [num_blocks, num_kv_heads, block_size * (head_dim / 2 + 4)]
+                           (codes, then a bf16 (scale, zero) pair per row; new_int4_cache)
 """
 
 from __future__ import annotations
@@ -35,6 +37,10 @@ __all__ = [
     "decode_split_noalloc", "swap_blocks", "reshape_and_cache_fp8", "decode_fp8", "decode_fp8_split",
     "prefill", "append_decode_kv", "append_decode_kv_fp8", "selftest_bounded_wait", "append_decode_kv_cow",
     "cow_sources", "prefix_groups", "decode_shared",
+    "int4_record_bytes", "new_int4_cache", "reshape_and_cache_int4", "append_decode_kv_int4",
+    "dequantize_blocks_int4", "decode_int4", "decode_int4_workspace_size", "new_int4_workspace",
+    "qk_norm_rope", "qk_norm_rope_cache", "qk_norm_rope_cache_fp8", "qk_norm_rope_cache_int4",
+    "prepare_batch", "release_blocks",
 ]
 
 
@@ -373,6 +379,284 @@ def decode_shared(query, key_cache, value_cache, block_tables, seq_lens, scale: 
     return out
 
 
+# ---- 4-bit cache ----------------------------------------------------------------------
+
+def _on_current(*tensors) -> None:
+    """The library launches on the current device: every tensor has to live there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != cur:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+
+
+def _rows(t, name: str, heads: int | None = None, head_dim: int | None = None, tokens: int | None = None):
+    """(pointer, token stride) of a bf16 [tokens, heads, head_dim] view whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
+    want = tuple(w if w is not None else n for w, n in zip((tokens, heads, head_dim), t.shape))
+    if tuple(t.shape) != want:
+        raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
+    row = t.shape[1] * t.shape[2]
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else row)
+
+
+def int4_record_bytes(block_size: int, head_dim: int) -> int:
+    """Bytes of one (block, KV head) record of a 4-bit cache."""
+    return int(block_size) * (int(head_dim) // 2 + 4)
+
+
+def new_int4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """A zero-filled 4-bit cache tensor (one of the two: keys or values)."""
+    return torch.zeros(num_blocks, num_kv_heads, int4_record_bytes(block_size, head_dim), dtype=torch.uint8,
+                       device=device)
+
+
+def _int4_dims(key_cache, value_cache, head_dim: int):
+    _dev(key_cache, torch.uint8, "key_cache", 3)
+    _dev(value_cache, torch.uint8, "value_cache", 3)
+    if key_cache.shape != value_cache.shape:
+        raise ValueError("key_cache and value_cache shapes differ")
+    nb, hkv, rec = key_cache.shape
+    if head_dim <= 0 or rec % (head_dim // 2 + 4) != 0:
+        raise ValueError(f"cache records of {rec} bytes do not hold rows of head_dim {head_dim}")
+    return nb, rec // (head_dim // 2 + 4), hkv
+
+
+def reshape_and_cache_int4(key, value, key_cache, value_cache, slot_mapping, stream=None) -> None:
+    """pa_reshape_and_cache_int4: bf16 rows (strided by token) quantised into 4-bit caches."""
+    k, ks = _rows(key, "key")
+    T, hkv, d = key.shape
+    nb, bs, heads = _int4_dims(key_cache, value_cache, d)
+    v, vs = _rows(value, "value", heads, d, T)
+    if hkv != heads:
+        raise ValueError("key/value must be [num_tokens, num_kv_heads, head_dim] matching the cache")
+    sm = _dev(slot_mapping, torch.int64, "slot_mapping", 1)
+    if slot_mapping.shape[0] != T:
+        raise ValueError("slot_mapping length != num_tokens")
+    _on_current(key, value, key_cache, value_cache, slot_mapping)
+    check("pa_reshape_and_cache_int4", load().pa_reshape_and_cache_int4(
+        k, v, ks, vs, key_cache.data_ptr(), value_cache.data_ptr(), sm, T, hkv, d, bs, nb, _stream(stream)))
+
+
+def append_decode_kv_int4(key, value, key_cache, value_cache, block_tables, seq_lens, slot_mapping=None,
+                          stream=None) -> None:
+    """pa_append_decode_kv_int4: as append_decode_kv into 4-bit caches."""
+    B = seq_lens.shape[0]
+    k, ks = _rows(key, "key", tokens=B)
+    _, hkv, d = key.shape
+    nb, bs, heads = _int4_dims(key_cache, value_cache, d)
+    v, vs = _rows(value, "value", heads, d, B)
+    if hkv != heads:
+        raise ValueError("key/value must be [num_seqs, num_kv_heads, head_dim] matching the cache")
+    bt = _dev(block_tables, torch.int32, "block_tables", 2)
+    if block_tables.shape[0] != B:
+        raise ValueError("block_tables rows != num_seqs")
+    sm = _dev(slot_mapping, torch.int64, "slot_mapping", 1)
+    if slot_mapping is not None and slot_mapping.shape[0] != B:
+        raise ValueError("slot_mapping length != num_seqs")
+    _on_current(key, value, key_cache, value_cache, block_tables, seq_lens, slot_mapping)
+    check("pa_append_decode_kv_int4", load().pa_append_decode_kv_int4(
+        k, v, ks, vs, key_cache.data_ptr(), value_cache.data_ptr(), bt, _dev(seq_lens, torch.int32, "seq_lens", 1),
+        sm, B, block_tables.shape[1], hkv, d, bs, nb, _stream(stream)))
+
+
+def dequantize_blocks_int4(key_cache, value_cache, block_ids, head_dim: int, *, key_out=None, value_out=None,
+                           stream=None):
+    """pa_dequantize_blocks_int4: the listed blocks as bf16 blocks [n, block_size, num_kv_heads, head_dim]."""
+    nb, bs, hkv = _int4_dims(key_cache, value_cache, head_dim)
+    ids = _dev(block_ids, torch.int32, "block_ids", 1)
+    shape = (block_ids.shape[0], bs, hkv, int(head_dim))
+    if key_out is None:
+        key_out = torch.zeros(shape, dtype=torch.bfloat16, device=key_cache.device)
+    if value_out is None:
+        value_out = torch.zeros(shape, dtype=torch.bfloat16, device=key_cache.device)
+    ko, vo = _dev(key_out, torch.bfloat16, "key_out", 4), _dev(value_out, torch.bfloat16, "value_out", 4)
+    if tuple(key_out.shape) != shape or tuple(value_out.shape) != shape:
+        raise ValueError(f"key_out / value_out must be {list(shape)}")
+    _on_current(key_cache, value_cache, block_ids, key_out, value_out)
+    check("pa_dequantize_blocks_int4", load().pa_dequantize_blocks_int4(
+        ko, vo, key_cache.data_ptr(), value_cache.data_ptr(), ids, shape[0], hkv, int(head_dim), bs, nb,
+        _stream(stream)))
+    return key_out, value_out
+
+
+def decode_int4_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of decode_int4 workspace; the same for every batch."""
+    return int(load().pa_decode_int4_workspace_size(num_heads, num_kv_heads, head_dim))
+
+
+def new_int4_workspace(num_heads: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """A zero-filled decode_int4 workspace (its counters must start at zero)."""
+    return torch.zeros(decode_int4_workspace_size(num_heads, num_kv_heads, head_dim), dtype=torch.uint8,
+                       device=device)
+
+
+def decode_int4(query, key_cache, value_cache, block_tables, seq_lens, scale: float, workspace, *, out=None,
+                stream=None):
+    """pa_decode_int4: single-query paged decode over 4-bit caches."""
+    q = _dev(query, torch.bfloat16, "query", 3)
+    B, hq, d = query.shape
+    nb, bs, hkv = _int4_dims(key_cache, value_cache, d)
+    bt = _dev(block_tables, torch.int32, "block_tables", 2)
+    sl = _dev(seq_lens, torch.int32, "seq_lens", 1)
+    if block_tables.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("block_tables / seq_lens batch size != query batch size")
+    o, out = _out(out, query)
+    if out.shape != query.shape:
+        raise ValueError("out must have the query's shape")
+    wp, wb = _ws(workspace)
+    _on_current(query, key_cache, value_cache, block_tables, seq_lens, out, workspace)
+    check("pa_decode_int4", load().pa_decode_int4(
+        o, q, key_cache.data_ptr(), value_cache.data_ptr(), bt, sl, float(scale), bs, hkv, B, hq, d,
+        block_tables.shape[1], nb, wp, wb, _stream(stream)))
+    return out
+
+
+# ---- head norm + rotation -------------------------------------------------------------
+
+def _rope_args(query, key, q_weight, k_weight, cos_sin, positions, query_out):
+    q, qs = _rows(query, "query")
+    T, hq, d = query.shape
+    k, ks = _rows(key, "key", head_dim=d, tokens=T)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _dev(w, torch.bfloat16, name, 1)
+        if w is not None and w.shape[0] != d:
+            raise ValueError(f"{name} must be [head_dim]")
+    cs = _dev(cos_sin, torch.float32, "cos_sin", 2)
+    ps = _dev(positions, torch.int64, "positions", 1)
+    if positions.shape[0] != T:
+        raise ValueError("positions length != num_tokens")
+    if query_out is None:
+        query_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=query.device)
+    qo, qos = _rows(query_out, "query_out", hq, d, T)
+    _on_current(query, key, q_weight, k_weight, cos_sin, positions, query_out)
+    w = [None if t is None else t.data_ptr() for t in (q_weight, k_weight)]
+    return T, hq, key.shape[1], d, q, qs, k, ks, qo, qos, query_out, w, cs, ps
+
+
+def qk_norm_rope(query, key, q_weight, k_weight, cos_sin, positions, *, eps: float = 1e-6, interleaved: bool = False,
+                 query_out=None, key_out=None, stream=None):
+    """pa_qk_norm_rope: RMS norm of every query and key head and position rotation.  Returns (query_out, key_out)."""
+    T, hq, hkv, d, q, qs, k, ks, qo, qos, query_out, w, cs, ps = _rope_args(query, key, q_weight, k_weight, cos_sin,
+                                                                            positions, query_out)
+    if key_out is None:
+        key_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=key.device)
+    ko, kos = _rows(key_out, "key_out", hkv, d, T)
+    _on_current(key_out)
+    check("pa_qk_norm_rope", load().pa_qk_norm_rope(
+        qo, ko, q, k, *w, cs, ps, float(eps), qos, kos, qs, ks, cos_sin.shape[1], int(bool(interleaved)),
+        cos_sin.shape[0], T, hq, hkv, d, _stream(stream)))
+    return query_out, key_out
+
+
+def _rope_cache(name, extra, query, key, value, q_weight, k_weight, cos_sin, positions, slot_mapping, key_cache,
+                value_cache, eps, interleaved, query_out, stream):
+    T, hq, hkv, d, q, qs, k, ks, qo, qos, query_out, w, cs, ps = _rope_args(query, key, q_weight, k_weight, cos_sin,
+                                                                            positions, query_out)
+    v, vs = _rows(value, "value", hkv, d, T)
+    if name.endswith("int4"):
+        nb, bs, heads = _int4_dims(key_cache, value_cache, d)
+        dim = d
+    else:
+        nb, bs, heads, dim = _cache_dims(key_cache, value_cache, torch.uint8 if extra else torch.bfloat16)
+    if (heads, dim) != (hkv, d):
+        raise ValueError("key/value must be [num_tokens, num_kv_heads, head_dim] matching the cache")
+    sm = _dev(slot_mapping, torch.int64, "slot_mapping", 1)
+    if slot_mapping.shape[0] != T:
+        raise ValueError("slot_mapping length != num_tokens")
+    _on_current(value, slot_mapping, key_cache, value_cache)
+    check(name, getattr(load(), name)(
+        qo, q, k, v, *w, cs, ps, sm, key_cache.data_ptr(), value_cache.data_ptr(), float(eps), qos, qs, ks, vs,
+        cos_sin.shape[1], int(bool(interleaved)), cos_sin.shape[0], T, hq, hkv, d, bs, nb, *extra, _stream(stream)))
+    return query_out
+
+
+def qk_norm_rope_cache(query, key, value, q_weight, k_weight, cos_sin, positions, slot_mapping, key_cache,
+                       value_cache, *, eps: float = 1e-6, interleaved: bool = False, query_out=None, stream=None):
+    """pa_qk_norm_rope_cache: qk_norm_rope with the keys and values written to bf16 caches.  Returns query_out."""
+    return _rope_cache("pa_qk_norm_rope_cache", (), query, key, value, q_weight, k_weight, cos_sin, positions,
+                       slot_mapping, key_cache, value_cache, eps, interleaved, query_out, stream)
+
+
+def qk_norm_rope_cache_fp8(query, key, value, q_weight, k_weight, cos_sin, positions, slot_mapping, key_cache,
+                           value_cache, k_scale: float, v_scale: float, *, eps: float = 1e-6,
+                           interleaved: bool = False, query_out=None, stream=None):
+    """pa_qk_norm_rope_cache_fp8: as qk_norm_rope_cache into E4M3 code caches."""
+    return _rope_cache("pa_qk_norm_rope_cache_fp8", (float(k_scale), float(v_scale)), query, key, value, q_weight,
+                       k_weight, cos_sin, positions, slot_mapping, key_cache, value_cache, eps, interleaved,
+                       query_out, stream)
+
+
+def qk_norm_rope_cache_int4(query, key, value, q_weight, k_weight, cos_sin, positions, slot_mapping, key_cache,
+                            value_cache, *, eps: float = 1e-6, interleaved: bool = False, query_out=None,
+                            stream=None):
+    """pa_qk_norm_rope_cache_int4: as qk_norm_rope_cache into 4-bit caches."""
+    return _rope_cache("pa_qk_norm_rope_cache_int4", (), query, key, value, q_weight, k_weight, cos_sin, positions,
+                       slot_mapping, key_cache, value_cache, eps, interleaved, query_out, stream)
+
+
+# ---- a step's tables and slots --------------------------------------------------------
+
+def _vec(t, dtype, name, n):
+    p = _dev(t, dtype, name, 1)
+    if t is not None and t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    return p
+
+
+def prepare_batch(block_tables, context_lens, query_lens, free_blocks, num_free, block_size: int, num_blocks: int, *,
+                  seq_lens, q_start, num_free_out, status, seq_ids=None, positions=None, slot_mapping=None,
+                  num_tokens: int | None = None, stream=None) -> None:
+    """pa_prepare_batch: new blocks, lengths, row starts, positions and slots of a ragged batch, on the device.
+
+    The outputs are the caller's tensors.  The per-token arrays (seq_ids int32, positions and slot_mapping int64)
+    are optional and of one length, the step's row capacity; num_tokens gives that capacity where none is passed."""
+    B = context_lens.shape[0]
+    bt = _dev(block_tables, torch.int32, "block_tables", 2)
+    if block_tables.shape[0] != B:
+        raise ValueError("block_tables rows != num_seqs")
+    per_token = [t for t in (seq_ids, positions, slot_mapping) if t is not None]
+    if num_tokens is None:
+        if not per_token:
+            raise ValueError("num_tokens is needed where no per-token array is passed")
+        num_tokens = per_token[0].shape[0]
+    n = int(num_tokens)
+    args = (bt, _dev(context_lens, torch.int32, "context_lens", 1), _vec(query_lens, torch.int32, "query_lens", B),
+            _dev(free_blocks, torch.int32, "free_blocks", 1), _vec(num_free, torch.int32, "num_free", 1),
+            _vec(seq_lens, torch.int32, "seq_lens", B), _vec(q_start, torch.int32, "q_start", B + 1),
+            _vec(seq_ids, torch.int32, "seq_ids", n), _vec(positions, torch.int64, "positions", n),
+            _vec(slot_mapping, torch.int64, "slot_mapping", n), _vec(num_free_out, torch.int32, "num_free_out", 1),
+            _vec(status, torch.int32, "status", 1))
+    _on_current(block_tables, context_lens, query_lens, free_blocks, num_free, seq_lens, q_start, num_free_out,
+                status, *per_token)
+    check("pa_prepare_batch", load().pa_prepare_batch(
+        *args, B, block_tables.shape[1], n, free_blocks.shape[0], int(block_size), int(num_blocks),
+        _stream(stream)))
+
+
+def release_blocks(block_tables, seq_lens, release, free_blocks, num_free, block_size: int, num_blocks: int, *,
+                   status, stream=None) -> None:
+    """pa_release_blocks: the blocks of the requests marked in `release` (int32) back on the free stack."""
+    B = seq_lens.shape[0]
+    bt = _dev(block_tables, torch.int32, "block_tables", 2)
+    if block_tables.shape[0] != B:
+        raise ValueError("block_tables rows != num_seqs")
+    args = (bt, _dev(seq_lens, torch.int32, "seq_lens", 1), _vec(release, torch.int32, "release", B),
+            _dev(free_blocks, torch.int32, "free_blocks", 1), _vec(num_free, torch.int32, "num_free", 1),
+            _vec(status, torch.int32, "status", 1))
+    _on_current(block_tables, seq_lens, release, free_blocks, num_free, status)
+    check("pa_release_blocks", load().pa_release_blocks(
+        *args, B, block_tables.shape[1], free_blocks.shape[0], int(block_size), int(num_blocks), _stream(stream)))
+
+
 # Bytes of the fixed scratch array inside the library (PA_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -458,5 +742,6 @@ def selftest_bounded_wait(stream=None) -> None:
 def device_status() -> int:
     """0, or a negative status: PA_ERR_DEVICE_TIMEOUT (-9) if a bounded device wait
     gave up, PA_ERR_VALUE_RANGE (-12) if the prefill read a value entry beyond the
-    fp16 range of its P.V operand.  Reading clears it."""
+    fp16 range of its P.V operand, PA_ERR_BAD_BLOCK (-7) if decode_int4 met a table
+    entry outside the cache.  Reading clears it."""
     return int(load().pa_device_status())
