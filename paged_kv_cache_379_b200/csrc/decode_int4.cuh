@@ -1,16 +1,26 @@
 // decode_int4.cuh -- single-query paged decode attention over a 4-bit cache
 // (format: row_ops.cuh).  With k_t = z_t + s_t c_t (scale, zero, codes of token
-// t's key row) and likewise for the values,
-//     x_t = scale * (s_t (q . c_t) + z_t sum(q)),   p_t = exp(x_t - m),
-//     out = (sum_t p_t s'_t c'_t + sum_t p_t z'_t) / sum_t p_t,
-// so a row's scale and zero meet its 64 bytes of codes only in per-token scalars.
+// t's key row) and v_t = z'_t + s'_t c'_t,
+//     x_t = scale * (s_t (q . c_t) + z_t sum(q)),   p_t = 2^(x_t log2 e - m),
+//     out = (sum_t (p_t s'_t) c'_t + sum_t p_t z'_t) / sum_t p_t,
+// so a row's scale and zero meet its codes only in per-token scalars, and the
+// codes go to the tensor cores as they are: a nibble in bits 0-3 of a half word
+// is the fp16 subnormal c 2^-24, one in bits 4-7 is 16 c 2^-24, so one AND turns
+// a 32-bit word into two exact fp16 operands; the 16 goes into the query (key
+// product) or out of the accumulator (value product).
 // Included once, by pagedkv.cu.
 #pragma once
 
 #include "common.cuh"
+#include "decode.cuh"
 #include "row_ops.cuh"
 
 namespace pakv {
+
+constexpr int kI4Warps = 4;
+constexpr int kI4Tokens = 32;        // tokens of one stage
+constexpr int kI4MaxWorkers = 592;   // CTAs with partial results: 148 SMs x 4
+constexpr int kI4HeaderBytes = 4096; // workspace: arrival counters of the workers
 
 struct Int4DecodeParams {
     __nv_bfloat16 *out;                 // [B, Hq, D]
@@ -18,93 +28,621 @@ struct Int4DecodeParams {
     const uint8_t *key_cache, *value_cache;
     const int32_t *block_tables;        // [B, max_blocks]
     const int32_t *seq_lens;            // [B]
-    void *workspace;
+    int *counters;                      // [workers], zero between calls
+    float2 *part_ml;                    // [2 workers][16] (m, l)
+    float4 *part_o;                     // [2 workers][NG * D/16 chunks][32 lanes]
     float scale_log2;                   // scale * log2(e)
-    int num_seqs, num_heads, num_kv_heads, group, max_blocks, num_blocks;
+    int num_seqs, num_heads, num_kv_heads, group, max_blocks, num_blocks, min_stages;
 };
 
-// One CTA per (KV head, sequence); warp w takes tokens w, w + 4, ...; a lane
-// holds D / 32 dims of every query head of the group.
-template <int D>
-__global__ void __launch_bounds__(128) decode_int4_simple_kernel(const Int4DecodeParams p, int block_size)
+template <int D, int BS, int NG>
+struct Int4Lay {
+    static constexpr int kRecs = kI4Tokens / BS;               // records of a stage, per cache
+    static constexpr int kRec = BS * (D / 2 + 4);
+    static constexpr int kStage = 2 * kRecs * kRec;            // K records, then V records
+    static constexpr int kSlots = D == 128 ? 3 : 5;            // stages in flight, per warp
+    static constexpr int kRing = kSlots * kStage;
+    static constexpr int kChunks = D / 16;                     // float4s a lane holds of 8 heads
+    static constexpr int kBytes = kI4Warps * kRing;
+    static constexpr int kCtas = NG == 1 ? 4 : 3;              // resident CTAs per SM
+    static_assert(kStage >= kChunks * 32 * 16, "a warp's result for 8 heads goes through one stage");
+    static_assert(kRec % 16 == 0 && kStage % 16 == 0, "bulk copies are multiples of 16 bytes");
+};
+
+// A run of stages [t0, t1) of one (sequence, KV head) unit in a worker's range.
+struct Int4Seg {
+    int s, h, len, nt, t0, t1, left;  // left: stages of the range from t0 on
+    unsigned pos;                     // index of t0 among all stages (its low bits pick the warp)
+};
+
+__device__ __forceinline__ int int4_len(const Int4DecodeParams &p, int s, int block_size)
 {
-    constexpr int E = D / 32;
-    constexpr int GMAX = 16;
-    __shared__ float sm_o[4][D], sm_m[4], sm_l[4];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.x, s = blockIdx.y;
+    return min(max(p.seq_lens[s], 0), p.max_blocks * block_size);
+}
+
+__device__ __forceinline__ int int4_stages(int len) { return (int)(((unsigned)len + kI4Tokens - 1) / kI4Tokens); }
+
+// Moves to the next unit of the range; false at its end.
+__device__ __forceinline__ bool int4_next(Int4Seg &g, const Int4DecodeParams &p, int block_size)
+{
+    const int n = g.t1 - g.t0;
+    g.pos += n;
+    g.left -= n;
+    if (g.left <= 0) return false;
+    if (++g.h == p.num_kv_heads) {
+        g.h = 0;
+        do {
+            if (++g.s >= p.num_seqs) return false;
+            g.len = int4_len(p, g.s, block_size);
+        } while (g.len == 0);
+        g.nt = int4_stages(g.len);
+    }
+    g.t0 = 0;
+    g.t1 = min(g.nt, g.left);
+    return true;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+// The worker of stage x when the stages are cut into ranges of q, the first r of
+// them one longer.
+__device__ __forceinline__ int int4_worker_of(int64_t x, int64_t q, int64_t r)
+{
+    const int64_t cut = r * (q + 1);
+    return (int)(x < cut ? x / (q + 1) : r + (x - cut) / q);
+}
+
+template <int D, int BS, int NG>
+__global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
+    decode_int4_kernel(const Int4DecodeParams p)
+{
+    using Lay = Int4Lay<D, BS, NG>;
+    constexpr int W = kI4Warps, NS = Lay::kSlots, RECS = Lay::kRecs, REC = Lay::kRec;
+    constexpr int KW = D / 32;    // words of a key row per lane (4 lanes a row)
+    constexpr int VW = D / 64;    // words of a value row per lane (8 lanes a row)
+    constexpr int MT = 4 * VW;    // 16-dim tiles of the output: a lane's 2 dims each
+    constexpr unsigned FULL = 0xffffffffu;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t s_bar[W * NS];
+    __shared__ float s_m[W][16], s_l[W][16];
+    __shared__ int64_t s_sum[W], s_start;
+    __shared__ int s_seq, s_last;
+    __shared__ unsigned s_active;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    const uint32_t ring = smem_u32(smem) + warp * Lay::kRing;
+    const uint32_t bars = smem_u32(s_bar) + warp * NS * 8;
+    if (lane == 0) {
+        for (int i = 0; i < NS; ++i) mbar_init(bars + 8 * i, 1);
+        fence_mbarrier_init();
+    }
+    if (tid == 0) s_seq = -1;
+
+    // ---- this worker's range of the stages, in (sequence, KV head, position) order
+    const int per = (p.num_seqs + W * 32 - 1) / (W * 32);
+    const int s_lo = min(tid * per, p.num_seqs), s_hi = min(s_lo + per, p.num_seqs);
+    int64_t mine = 0;
+    for (int s = s_lo; s < s_hi; ++s) mine += int4_stages(int4_len(p, s, BS));
+    int64_t scan = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t v = __shfl_up_sync(FULL, scan, off);
+        if (lane >= off) scan += v;
+    }
+    if (lane == 31) s_sum[warp] = scan;
+    __syncthreads();
+    int64_t total = 0, before = scan - mine;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) before += s_sum[w];
+        total += s_sum[w];
+    }
+    before *= p.num_kv_heads;
+    total *= p.num_kv_heads;
+    const int workers = (int)min((int64_t)gridDim.x, max((int64_t)1, total / p.min_stages));
+    const int64_t quot = total / workers, rest = total - quot * workers;
+    const int me = blockIdx.x;
+    const int64_t lo = me * quot + min((int64_t)me, rest);
+    const int range = me < workers ? (int)(quot + (me < rest ? 1 : 0)) : 0;
+    if (range > 0 && lo >= before && lo < before + mine * p.num_kv_heads) {
+        int64_t at = before;
+        for (int s = s_lo; s < s_hi; ++s) {
+            const int64_t n = (int64_t)int4_stages(int4_len(p, s, BS)) * p.num_kv_heads;
+            if (lo < at + n) {
+                s_seq = s;
+                s_start = at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+
+    Int4Seg seg = {};
+    seg.s = s_seq;
+    bool more = seg.s >= 0;
+    int64_t unit0 = 0;  // index of the current unit's first stage
+    if (more) {
+        seg.len = int4_len(p, seg.s, BS);
+        seg.nt = int4_stages(seg.len);
+        seg.h = (int)((lo - s_start) / seg.nt);
+        seg.t0 = (int)(lo - s_start - (int64_t)seg.h * seg.nt);
+        seg.left = range;
+        seg.t1 = min(seg.nt, seg.t0 + range);
+        seg.pos = (unsigned)lo;
+        unit0 = lo - seg.t0;
+    }
+
+    // ---- the copies: this warp's next stage, its table entries fetched one stage ahead
+    Int4Seg ps = seg;
+    int pt = 0, ent = 0;
+    bool pvalid = more;
+    unsigned badmask = 0;
+    auto settle = [&] {  // pt past its segment: on to the next one that has a stage for this warp
+        while (pvalid && pt >= ps.t1) {
+            pvalid = int4_next(ps, p, BS);
+            if (pvalid) pt = ps.t0 + ((warp - ps.pos) & (W - 1));
+        }
+        if (pvalid && lane < 2 * RECS) {
+            const int i = pt * RECS + (lane >> 1);
+            if (i * BS < ps.len) ent = p.block_tables[(int64_t)ps.s * p.max_blocks + i];
+        }
+    };
+    auto issue = [&](int slot) {
+        if (!pvalid) return;
+        const int recs = min(RECS, (ps.len - pt * kI4Tokens + BS - 1) / BS);
+        const bool act = lane < 2 * recs;
+        const bool bad = act && (ent < 0 || ent >= p.num_blocks);
+        if (bad) {
+            record_status(kStatusBadBlock);
+            ent = 0;  // block 0 stands in; the result becomes NaN
+        }
+        badmask = (badmask & ~(1u << slot)) | ((__ballot_sync(FULL, bad) != 0 ? 1u : 0u) << slot);
+        if (lane == 0) mbar_arrive_expect_tx(bars + 8 * slot, recs * 2 * REC);
+        __syncwarp();
+        if (act) {
+            const int64_t rec = ((int64_t)ent * p.num_kv_heads + ps.h) * REC;
+            bulk_load(ring + slot * Lay::kStage + ((lane & 1) * RECS + (lane >> 1)) * REC,
+                      ((lane & 1) ? p.value_cache : p.key_cache) + rec, REC, bars + 8 * slot);
+        }
+        pt += W;
+        settle();
+    };
+    if (more) pt = seg.t0 + ((warp - seg.pos) & (W - 1));
+    settle();
     pdl_wait();
-    const int L = min(p.seq_lens[s], p.max_blocks * block_size);
-    const int G = p.group;
-    const __nv_bfloat16 *q = p.query + ((int64_t)s * p.num_heads + (int64_t)h * G) * D + lane * E;
-    float qf[GMAX][E], o[GMAX][E], m[GMAX], l[GMAX];
-#pragma unroll
-    for (int g = 0; g < GMAX; ++g) {
-        m[g] = -INFINITY;
-        l[g] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            o[g][e] = 0.f;
-            qf[g][e] = g < G ? __bfloat162float(q[g * D + e]) * p.scale_log2 : 0.f;
+    pdl_launch_dependents();
+    int issued = 0;
+    for (; issued < NS && pvalid; ++issued) issue(issued);
+
+    // rows of sequences without a token
+    for (int s = me; s < p.num_seqs; s += gridDim.x)
+        if (p.seq_lens[s] <= 0) {
+            uint4 *row = reinterpret_cast<uint4 *>(p.out + (int64_t)s * p.num_heads * D);
+            for (int i = tid; i < p.num_heads * D / 8; i += W * 32) row[i] = make_uint4(0u, 0u, 0u, 0u);
         }
-    }
-    for (int t = warp; t < L; t += 4) {
-        const int block = p.block_tables[(int64_t)s * p.max_blocks + t / block_size];
-        const bool bad = block < 0 || block >= p.num_blocks;
-        if (bad) record_status(kStatusBadBlock);
-        const int row = t % block_size;
-        const int64_t rec = ((int64_t)(bad ? 0 : block) * p.num_kv_heads + h) * int4_record_bytes(block_size, D);
-        float kf[E], vf[E];
+
+    // token of row r of an 8-token group: the order that spreads the value rows over the banks
+    constexpr uint32_t PERM = D == 128 ? 0x67542310u : 0x57463120u;
+    const int krow = (PERM >> (4 * g)) & 7;
+    const int vrow0 = (PERM >> (8 * c)) & 7, vrow1 = (PERM >> (8 * c + 4)) & 7;
+    constexpr int RB = D / 2;  // bytes of a row
+    // offset of token `row` (0..7) of 8-token group q (0..3) of a stage
+    auto row_at = [&](int q, int row) { return BS == 8 ? q * REC + row * RB
+                                             : BS == 16 ? (q >> 1) * REC + ((q & 1) * 8 + row) * RB
+                                                        : (q * 8 + row) * RB; };
+    auto pair_at = [&](int q, int row) { return BS == 8 ? q * REC + BS * RB + row * 4
+                                              : BS == 16 ? (q >> 1) * REC + BS * RB + ((q & 1) * 8 + row) * 4
+                                                         : BS * RB + (q * 8 + row) * 4; };
+
+    int arrived = 0, slot = 0;
+    uint32_t phase = 0;
+    bool dead = false;  // a wait gave up: nothing more is copied or waited for
+    while (more) {
+        // ---- the unit's queries: fp16, each head scaled by a power of two (its largest
+        // magnitude into [2^14, 2^15)), exact within 2^27 of that
+        uint32_t qf[NG][KW][4];
+        float qa[NG][2], qb[NG][2];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            const uint8_t *r = (kv ? p.value_cache : p.key_cache) + rec;
-            const float2 sz = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(r + block_size * (D / 2) + row * 4));
+        for (int n = 0; n < NG; ++n) {
+            const int head = n * 8 + g;
+            uint4 raw[KW];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const uint8_t byte = r[row * (D / 2) + (lane * E + e) / 2];
-                (kv ? vf : kf)[e] = bad ? NAN : fmaf(sz.x, (float)((byte >> (4 * (e & 1))) & 15), sz.y);
+            for (int j = 0; j < KW; ++j) {
+                raw[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (head < p.group)
+                    raw[j] = *reinterpret_cast<const uint4 *>(
+                        p.query + ((int64_t)seg.s * p.num_heads + seg.h * p.group + head) * D + c * (D / 4) + 8 * j);
+            }
+            uint32_t top = 0;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < KW; ++j) {
+                float x[8];
+                unpack8(raw[j], x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+                    sum += x[e];
+                }
+            }
+#pragma unroll
+            for (int off = 1; off <= 2; off <<= 1) {
+                top = max(top, __shfl_xor_sync(FULL, top, off));
+                sum += __shfl_xor_sync(FULL, sum, off);
+            }
+            const int e = max((int)(top >> 23) - 127, -100);
+            const float mul = pow2i(max(14 - e, -126));
+#pragma unroll
+            for (int j = 0; j < KW; ++j) {
+                float x[8];
+                unpack8(raw[j], x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] *= mul;
+                qf[n][j][0] = pack_f16x2(x[0], x[4]);
+                qf[n][j][1] = pack_f16x2(x[1] * 0.0625f, x[5] * 0.0625f);
+                qf[n][j][2] = pack_f16x2(x[2], x[6]);
+                qf[n][j][3] = pack_f16x2(x[3] * 0.0625f, x[7] * 0.0625f);
+            }
+            // logit = (s S) qa + z qb; an infinity or a NaN in the query makes both NaN
+            float a = p.scale_log2 * 1024.f * pow2i(min(e, 127)), b = p.scale_log2 * sum;
+            if (top >= 0x7F800000u) a = b = __uint_as_float(0x7FC00000u);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                qa[n][i] = __shfl_sync(FULL, a, (2 * c + i) * 4);
+                qb[n][i] = __shfl_sync(FULL, b, (2 * c + i) * 4);
             }
         }
+
+        float o[NG][MT][4], m[NG][2], l[NG][2], zs[NG][2];
 #pragma unroll
-        for (int g = 0; g < GMAX; ++g) {
-            if (g >= G) break;
-            float x = 0.f;
+        for (int n = 0; n < NG; ++n) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) x = fmaf(qf[g][e], kf[e], x);
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-            const float mn = fmaxf(m[g], x);
-            const float corr = m[g] == -INFINITY ? 0.f : exp2f(m[g] - mn);
-            const float w = exp2f(x - mn);
-            m[g] = mn;
-            l[g] = l[g] * corr + w;
+                for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[g][e] = fmaf(w, vf[e], o[g][e] * corr);
-        }
-    }
-#pragma unroll
-    for (int g = 0; g < GMAX; ++g) {
-        if (g >= G) break;
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = o[g][e];
-        if (lane == 0) {
-            sm_m[warp] = m[g];
-            sm_l[warp] = l[g];
-        }
-        __syncthreads();
-        const float M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-        if (threadIdx.x < D) {
-            float acc = 0.f, den = 0.f;
-            for (int w = 0; w < 4; ++w) {
-                if (sm_l[w] == 0.f) continue;  // a warp without a token
-                const float c = exp2f(sm_m[w] - M);
-                den = fmaf(c, sm_l[w], den);
-                acc = fmaf(c, sm_o[w][threadIdx.x], acc);
+            for (int i = 0; i < 2; ++i) {
+                m[n][i] = -INFINITY;
+                l[n][i] = zs[n][i] = 0.f;
             }
-            p.out[((int64_t)s * p.num_heads + (int64_t)h * G + g) * D + threadIdx.x] =
-                __float2bfloat16_rn(den == 0.f ? 0.f : acc / den);
         }
+        int ev = -1000;       // value scales of this unit are below 2^(ev + 1) so far
+        float vmul = 0.f;     // 2^(10 - ev)
+        bool active = false;
+        int freed = -1;       // the slot of this warp's last stage of the segment
+        bool poison = false;
+
+        for (int t = seg.t0 + ((warp - seg.pos) & (W - 1)); t < seg.t1; t += W) {
+            if (!dead) {
+                dead = !__all_sync(FULL, mbar_wait_bounded(bars + 8 * slot, phase));
+                if (dead)
+                    record_timeout(kTimeoutFullBarrier);
+                else
+                    ++arrived;
+            }
+            poison |= dead || ((badmask >> slot) & 1u);
+            active = true;
+            const uint32_t kb = ring + slot * Lay::kStage, vb = kb + RECS * REC;
+
+            // ---- S = codes . q: 16 tokens x 8 heads x 16 dims a step
+            float sc[2][NG][4];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
+                uint32_t k0[KW], k1[KW];
+                const uint32_t a0 = kb + row_at(2 * mt, krow) + c * (D / 8);
+                const uint32_t a1 = kb + row_at(2 * mt + 1, krow) + c * (D / 8);
+                if constexpr (KW == 4) {
+                    const uint4 u = lds128(a0), v = lds128(a1);
+                    k0[0] = u.x, k0[1] = u.y, k0[2] = u.z, k0[3] = u.w;
+                    k1[0] = v.x, k1[1] = v.y, k1[2] = v.z, k1[3] = v.w;
+                } else {
+                    const uint2 u = lds64(a0), v = lds64(a1);
+                    k0[0] = u.x, k0[1] = u.y;
+                    k1[0] = v.x, k1[1] = v.y;
+                }
+#pragma unroll
+                for (int j = 0; j < KW; ++j) {
+                    const uint32_t u = k0[j], v = k1[j], u8 = u >> 8, v8 = v >> 8;
+#pragma unroll
+                    for (int n = 0; n < NG; ++n) {
+                        mma_f16_16816(sc[mt][n], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
+                                      qf[n][j][0], qf[n][j][1]);
+                        mma_f16_16816(sc[mt][n], u8 & 0x000F000Fu, v8 & 0x000F000Fu, u8 & 0x00F000F0u,
+                                      v8 & 0x00F000F0u, qf[n][j][2], qf[n][j][3]);
+                    }
+                }
+            }
+
+            // ---- logits and the rows' pairs; row g + 8 * half of tile mt is token 8 (2 mt + half) + krow
+            float2 vp[4];
+            const bool tail = (t + 1) * kI4Tokens > seg.len;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 kp = unpack_bf16x2(lds32(kb + pair_at(q, krow)));
+                vp[q] = unpack_bf16x2(lds32(vb + pair_at(q, krow)));
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &x = sc[q >> 1][n][(q & 1) * 2 + i];
+                        x = fmaf(kp.x * x, qa[n][i], kp.y * qb[n][i]);
+                    }
+            }
+            if (tail) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (t * kI4Tokens + q * 8 + krow >= seg.len) {
+                        vp[q] = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int n = 0; n < NG; ++n) sc[q >> 1][n][(q & 1) * 2] = sc[q >> 1][n][(q & 1) * 2 + 1] = -INFINITY;
+                    }
+            }
+
+            // ---- running maximum and value scale, moved only when a logit passes the
+            // maximum by more than 4 (so a weight stays below 2^4) or a scale its bound
+            bool move = false;
+            float vtop = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                vtop = fmaxf(vtop, vp[q].x);
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) move |= sc[q >> 1][n][(q & 1) * 2 + i] > m[n][i] + 4.f;
+            }
+            const int ve = (int)(__float_as_uint(vtop) >> 23) - 127;
+            move |= ve > ev;
+            if (__any_sync(FULL, move)) {
+                const int en = max(max(ev, __reduce_max_sync(FULL, ve)), -100);
+                const float vcorr = exp2f((float)(ev - en));
+                ev = en;
+                vmul = pow2i(10 - en);
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float top = m[n][i];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) top = fmaxf(top, sc[q >> 1][n][(q & 1) * 2 + i]);
+#pragma unroll
+                        for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, off));
+                        const float corr = m[n][i] == -INFINITY ? 0.f : exp2f(m[n][i] - top);
+                        m[n][i] = top;
+                        l[n][i] *= corr;  // a NaN stays one
+                        zs[n][i] *= corr;
+                        const float oc = corr * vcorr;
+#pragma unroll
+                        for (int k = 0; k < MT; ++k) {
+                            o[n][k][i] *= oc;
+                            o[n][k][2 + i] *= oc;
+                        }
+                    }
+            }
+
+            // ---- weights: fp32 into l and the zeros' sum; times the value scale and rounded
+            // to fp16 (2^-11 relative) for the tensor cores, one 8x8 transpose each
+            uint32_t pf[NG][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float vs = vp[q].x * vmul;
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    float w[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float pr = fast_exp2(sc[q >> 1][n][(q & 1) * 2 + i] - m[n][i]);
+                        l[n][i] += pr;
+                        zs[n][i] = fmaf(pr, vp[q].y, zs[n][i]);
+                        w[i] = pr * vs;
+                    }
+                    pf[n][q] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+                }
+            }
+
+            // ---- O += codes' . w: 16 dims x 8 heads x 16 tokens a step
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+                uint32_t v[4][VW];  // tokens vrow0, vrow1 of group 2 mt, then of 2 mt + 1
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a = vb + row_at(2 * mt + (i >> 1), (i & 1) ? vrow1 : vrow0) + g * (D / 16);
+                    if constexpr (VW == 2) {
+                        const uint2 u = lds64(a);
+                        v[i][0] = u.x, v[i][1] = u.y;
+                    } else {
+                        v[i][0] = lds32(a);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < VW; ++w)
+#pragma unroll
+                    for (int hw = 0; hw < 2; ++hw) {
+                        const uint32_t sel = hw ? 0x7632u : 0x5410u;
+                        const uint32_t x = prmt(v[0][w], v[1][w], sel), y = prmt(v[2][w], v[3][w], sel);
+                        const uint32_t x8 = x >> 8, y8 = y >> 8;
+#pragma unroll
+                        for (int n = 0; n < NG; ++n) {
+                            mma_f16_16816(o[n][4 * w + 2 * hw], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu,
+                                          y & 0x00F000F0u, pf[n][2 * mt], pf[n][2 * mt + 1]);
+                            mma_f16_16816(o[n][4 * w + 2 * hw + 1], x8 & 0x000F000Fu, x8 & 0x00F000F0u,
+                                          y8 & 0x000F000Fu, y8 & 0x00F000F0u, pf[n][2 * mt], pf[n][2 * mt + 1]);
+                        }
+                    }
+            }
+
+            // ---- hand the slot back; the segment's last one first carries the result
+            __syncwarp();
+            if (t + W < seg.t1) {
+                if (!dead && pvalid) {
+                    issue(slot);
+                    ++issued;
+                }
+            } else {
+                freed = slot;
+            }
+            if (++slot == NS) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+
+        // ---- join the four warps: result of 8 heads at a time, [chunk][lane] float4s;
+        // chunk k of a lane: head 2c + k / (chunks / 2), dims g D/8 + 4 (k % (chunks / 2)) ..
+        const bool whole = seg.t0 == 0 && seg.t1 == seg.nt;
+        int first = me, last = me;
+        if (!whole) {
+            first = seg.t0 == 0 ? me : int4_worker_of(unit0, quot, rest);
+            last = seg.t1 == seg.nt ? me : int4_worker_of(unit0 + seg.nt - 1, quot, rest);
+        }
+        const int64_t part = 2 * (int64_t)me + (seg.t0 == 0 ? 1 : 0);
+        if (tid == 0) s_active = 0;
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            if (active) {
+                if (n == 0 && lane == 0) atomicOr(&s_active, 1u << warp);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int off = 4; off <= 16; off <<= 1) {
+                        l[n][i] += __shfl_xor_sync(FULL, l[n][i], off);
+                        zs[n][i] += __shfl_xor_sync(FULL, zs[n][i], off);
+                    }
+                    if (poison) l[n][i] = __uint_as_float(0x7FC00000u);
+                    if (g == 0) {
+                        s_m[warp][n * 8 + 2 * c + i] = m[n][i];
+                        s_l[warp][n * 8 + 2 * c + i] = l[n][i];
+                    }
+                    const float f = pow2i(ev);  // out of the accumulators: 2^24 2^(ev - 10)
+#pragma unroll
+                    for (int k = 0; k < MT / 2; ++k) {
+                        const float4 r = make_float4(
+                            fmaf(o[n][2 * k][i] * 16384.f, f, zs[n][i]), fmaf(o[n][2 * k][2 + i] * 1024.f, f, zs[n][i]),
+                            fmaf(o[n][2 * k + 1][i] * 16384.f, f, zs[n][i]),
+                            fmaf(o[n][2 * k + 1][2 + i] * 1024.f, f, zs[n][i]));
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         ring + freed * Lay::kStage + ((i * (MT / 2) + k) * 32 + lane) * 16),
+                                     "f"(r.x), "f"(r.y), "f"(r.z), "f"(r.w)
+                                     : "memory");
+                    }
+                }
+            }
+            // where each warp keeps its result: slots differ, so they are passed along
+            if (lane == 0) s_sum[warp] = (int64_t)(active ? warp * Lay::kRing + freed * Lay::kStage : 0);
+            __syncthreads();
+            const unsigned act = s_active;
+#pragma unroll
+            for (int k = warp; k < Lay::kChunks; k += W) {
+                const int hd = n * 8 + 2 * c + k / (Lay::kChunks / 2);
+                const int dim = g * (D / 8) + 4 * (k % (Lay::kChunks / 2));
+                if (hd >= p.group) continue;
+                float M = -INFINITY, L = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < W; ++w)
+                    if ((act >> w) & 1u) M = fmaxf(M, s_m[w][hd]);
+#pragma unroll
+                for (int w = 0; w < W; ++w)
+                    if ((act >> w) & 1u) {
+                        const float f = exp2f(s_m[w][hd] - M);
+                        const float4 r = *reinterpret_cast<const float4 *>(smem + s_sum[w] + (k * 32 + lane) * 16);
+                        L = fmaf(f, s_l[w][hd], L);
+                        acc.x = fmaf(f, r.x, acc.x);
+                        acc.y = fmaf(f, r.y, acc.y);
+                        acc.z = fmaf(f, r.z, acc.z);
+                        acc.w = fmaf(f, r.w, acc.w);
+                    }
+                if (whole) {
+                    const float inv = 1.f / L;
+                    *reinterpret_cast<uint2 *>(
+                        p.out + ((int64_t)seg.s * p.num_heads + seg.h * p.group + hd) * D + dim) =
+                        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                } else {
+                    p.part_o[(part * NG + n) * (Lay::kChunks * 32) + k * 32 + lane] = acc;
+                    if (g == 0 && k % (Lay::kChunks / 2) == 0) p.part_ml[part * 16 + hd] = make_float2(M, L);
+                }
+            }
+            __syncthreads();
+        }
+
+        // ---- a unit cut between workers: the last one to arrive joins its parts, in order
+        if (!whole) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int n = last - first;  // arrivals before the last one
+                const int old = atomicAdd(p.counters + first, 1);
+                s_last = old == n;
+                if (old == n) p.counters[first] = 0;
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+                    for (int k = warp; k < Lay::kChunks; k += W) {
+                        const int hd = n * 8 + 2 * c + k / (Lay::kChunks / 2);
+                        const int dim = g * (D / 8) + 4 * (k % (Lay::kChunks / 2));
+                        if (hd >= p.group) continue;
+                        float M = -INFINITY, L = 0.f;
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                        for (int w = first; w <= last; ++w)
+                            M = fmaxf(M, __ldcg(&p.part_ml[(2 * w + (w == first ? 1 : 0)) * 16 + hd]).x);
+#pragma unroll 8
+                        for (int w = first; w <= last; ++w) {
+                            const int64_t q = 2 * w + (w == first ? 1 : 0);
+                            const float2 ml = __ldcg(&p.part_ml[q * 16 + hd]);
+                            const float4 r = __ldcg(&p.part_o[(q * NG + n) * (Lay::kChunks * 32) + k * 32 + lane]);
+                            const float f = exp2f(ml.x - M);
+                            L = fmaf(f, ml.y, L);
+                            acc.x = fmaf(f, r.x, acc.x);
+                            acc.y = fmaf(f, r.y, acc.y);
+                            acc.z = fmaf(f, r.z, acc.z);
+                            acc.w = fmaf(f, r.w, acc.w);
+                        }
+                        const float inv = 1.f / L;
+                        *reinterpret_cast<uint2 *>(
+                            p.out + ((int64_t)seg.s * p.num_heads + seg.h * p.group + hd) * D + dim) =
+                            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                    }
+            }
+        }
+
+        // ---- the kept slot can be filled again (its last readers and writers were generic)
+        if (freed >= 0 && !dead && pvalid) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            issue(freed);
+            ++issued;
+        }
+        unit0 += seg.nt;
+        more = int4_next(seg, p, BS);
+    }
+    // a warp that gave up still waits, bounded, for the copies it has in flight
+    if (dead) {
+        for (int i = arrived; i < issued; ++i)
+            if (!mbar_wait_bounded(bars + 8 * (i % NS), (i / NS) & 1)) record_timeout(kTimeoutDrain);
     }
 }
 

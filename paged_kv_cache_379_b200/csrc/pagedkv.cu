@@ -483,6 +483,54 @@ static int write_int4(const void *key, const void *value, int64_t key_stride, in
     return launch_rows<kCacheInt4, false>(p, head_dim, num_tokens, false, static_cast<cudaStream_t>(stream));
 }
 
+// 4-bit decode workspace: arrival counters, (m, l) and the results of two cut
+// units per worker.  Groups of more than 8 query heads hold twice the result and
+// run 3 instead of 4 CTAs per SM.
+struct Int4Workspace {
+    int workers;
+    size_t part_o, bytes;
+};
+static Int4Workspace int4_workspace(int group, int head_dim)
+{
+    Int4Workspace w;
+    const int ng = group > 8 ? 2 : 1;
+    w.workers = ng == 1 ? kI4MaxWorkers : kI4MaxWorkers / 4 * 3;
+    w.part_o = kI4HeaderBytes + (size_t)w.workers * 2 * 16 * sizeof(float2);
+    w.bytes = w.part_o + (size_t)w.workers * 2 * ng * 8 * head_dim * sizeof(float);
+    return w;
+}
+
+// Fewest stages (32 tokens of one KV head) worth a worker of its own.
+static constexpr int kI4MinStages = 4;
+
+template <int D, int BS, int NG>
+static int launch_decode_int4_t(const Int4DecodeParams &p, int workers, cudaStream_t st)
+{
+    using Lay = Int4Lay<D, BS, NG>;
+    auto kernel = decode_int4_kernel<D, BS, NG>;
+    const int rc = ensure_smem(reinterpret_cast<const void *>(kernel), Lay::kBytes);
+    if (rc != PA_OK) return rc;
+    const int sms = sm_count();
+    if (sms < 1) return check_cuda(cudaErrorInvalidConfiguration);
+    const int64_t most = (int64_t)p.num_seqs * p.num_kv_heads * cdiv64((int64_t)p.max_blocks * BS, kI4Tokens);
+    const int64_t grid = std::min<int64_t>({workers, (int64_t)sms * Lay::kCtas, cdiv64(most, p.min_stages)});
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(kI4Warps * 32), Lay::kBytes, st, p);
+}
+
+template <int D>
+static int launch_decode_int4_d(int block_size, const Int4DecodeParams &p, int workers, cudaStream_t st)
+{
+    switch (block_size * 2 + (p.group > 8)) {
+    case 16: return launch_decode_int4_t<D, 8, 1>(p, workers, st);
+    case 17: return launch_decode_int4_t<D, 8, 2>(p, workers, st);
+    case 32: return launch_decode_int4_t<D, 16, 1>(p, workers, st);
+    case 33: return launch_decode_int4_t<D, 16, 2>(p, workers, st);
+    case 64: return launch_decode_int4_t<D, 32, 1>(p, workers, st);
+    case 65: return launch_decode_int4_t<D, 32, 2>(p, workers, st);
+    default: return PA_ERR_UNSUPPORTED;
+    }
+}
+
 // The arguments the four pa_qk_norm_rope* entry points share.
 static int rope_params(RowParams &p, void *query_out, const void *query, const void *key, const void *q_weight,
                        const void *k_weight, const float *cos_sin, const int64_t *positions, float eps,
@@ -1200,7 +1248,7 @@ int pa_qk_norm_rope_cache_int4(void *query_out, const void *query, const void *k
 size_t pa_decode_int4_workspace_size(int num_heads, int num_kv_heads, int head_dim)
 {
     if (num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_heads % num_kv_heads != 0) return 0;
-    return kSchedBytes;
+    return int4_workspace(num_heads / num_kv_heads, head_dim).bytes;
 }
 
 int pa_decode_int4(void *out, const void *query, const void *key_cache, const void *value_cache,
@@ -1217,9 +1265,8 @@ int pa_decode_int4(void *out, const void *query, const void *key_cache, const vo
     if (num_seqs == 0) return PA_OK;
     if (!out || !query || !block_tables || !seq_lens) return PA_ERR_NULL_POINTER;
     if (!aligned16(out) || !aligned16(query)) return PA_ERR_ALIGNMENT;
-    if (!workspace || !aligned16(workspace) ||
-        workspace_bytes < pa_decode_int4_workspace_size(num_heads, num_kv_heads, head_dim))
-        return PA_ERR_WORKSPACE;
+    const Int4Workspace lay = int4_workspace(num_heads / num_kv_heads, head_dim);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < lay.bytes) return PA_ERR_WORKSPACE;
     if (num_seqs > 65535) return PA_ERR_BAD_SHAPE;
     Int4DecodeParams p = {};
     p.out = static_cast<__nv_bfloat16 *>(out);
@@ -1228,7 +1275,9 @@ int pa_decode_int4(void *out, const void *query, const void *key_cache, const vo
     p.value_cache = static_cast<const uint8_t *>(value_cache);
     p.block_tables = block_tables;
     p.seq_lens = seq_lens;
-    p.workspace = workspace;
+    p.counters = static_cast<int *>(workspace);
+    p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + kI4HeaderBytes);
+    p.part_o = reinterpret_cast<float4 *>(static_cast<char *>(workspace) + lay.part_o);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.num_seqs = num_seqs;
     p.num_heads = num_heads;
@@ -1236,9 +1285,10 @@ int pa_decode_int4(void *out, const void *query, const void *key_cache, const vo
     p.group = num_heads / num_kv_heads;
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = num_blocks;
-    return launch_pdl(head_dim == 64 ? decode_int4_simple_kernel<64> : decode_int4_simple_kernel<128>,
-                      dim3((unsigned)num_kv_heads, (unsigned)num_seqs), dim3(128), 0,
-                      static_cast<cudaStream_t>(stream), p, block_size);
+    p.min_stages = kI4MinStages;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return head_dim == 64 ? launch_decode_int4_d<64>(block_size, p, lay.workers, st)
+                          : launch_decode_int4_d<128>(block_size, p, lay.workers, st);
 }
 
 // ----------------------------------------------------------- a step's tables and slots
