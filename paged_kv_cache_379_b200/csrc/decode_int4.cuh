@@ -46,13 +46,18 @@ struct Int4Lay {
     static constexpr int kBytes = kI4Warps * kRing;
     static constexpr int kCtas = NG == 1 ? 4 : 3;              // resident CTAs per SM
     static_assert(kStage >= kChunks * 32 * 16, "a warp's result for 8 heads goes through one stage");
+    static_assert(kStage >= kI4Warps * 32 * 16 + 8 * (kI4Warps * 32 / (D / 4)), "and a join of shared parts");
     static_assert(kRec % 16 == 0 && kStage % 16 == 0, "bulk copies are multiples of 16 bytes");
 };
 
-// A run of stages [t0, t1) of one (sequence, KV head) unit in a worker's range.
+// A unit (sequence, KV head) of nt stages weighs nt + kI4UnitCost stages when the
+// work is cut into ranges: what its queries' set-up and the join of its results take.
+constexpr int kI4UnitCost = 6;
+
+// A run of stages [t0, t1) of one unit in a worker's range.
 struct Int4Seg {
-    int s, h, len, nt, t0, t1, left;  // left: stages of the range from t0 on
-    unsigned pos;                     // index of t0 among all stages (its low bits pick the warp)
+    int s, h, len, nt, t0, t1, left;  // left: weight of the range behind this unit (negative: it ends in here)
+    unsigned pos;                     // stages of the range before t0 (the low bits pick the warp)
 };
 
 __device__ __forceinline__ int int4_len(const Int4DecodeParams &p, int s, int block_size)
@@ -62,13 +67,13 @@ __device__ __forceinline__ int int4_len(const Int4DecodeParams &p, int s, int bl
 
 __device__ __forceinline__ int int4_stages(int len) { return (int)(((unsigned)len + kI4Tokens - 1) / kI4Tokens); }
 
+__device__ __forceinline__ int int4_weight(int len) { return len > 0 ? int4_stages(len) + kI4UnitCost : 0; }
+
 // Moves to the next unit of the range; false at its end.
 __device__ __forceinline__ bool int4_next(Int4Seg &g, const Int4DecodeParams &p, int block_size)
 {
-    const int n = g.t1 - g.t0;
-    g.pos += n;
-    g.left -= n;
-    if (g.left <= 0) return false;
+    g.pos += g.t1 - g.t0;
+    if (g.left <= kI4UnitCost) return false;
     if (++g.h == p.num_kv_heads) {
         g.h = 0;
         do {
@@ -78,28 +83,25 @@ __device__ __forceinline__ bool int4_next(Int4Seg &g, const Int4DecodeParams &p,
         g.nt = int4_stages(g.len);
     }
     g.t0 = 0;
-    g.t1 = min(g.nt, g.left);
+    g.t1 = min(g.nt, g.left - kI4UnitCost);
+    g.left -= g.nt + kI4UnitCost;
     return true;
 }
 
-__device__ __forceinline__ uint2 lds64(uint32_t addr)
+// mma_f16_16816 without `volatile`: the compiler may interleave independent ones.
+__device__ __forceinline__ void mma_codes(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
 {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
-// The worker of stage x when the stages are cut into ranges of q, the first r of
-// them one longer.
+// The worker of position x when the weight is cut into ranges of q, the first r
+// of them one longer.
 __device__ __forceinline__ int int4_worker_of(int64_t x, int64_t q, int64_t r)
 {
     const int64_t cut = r * (q + 1);
@@ -118,14 +120,14 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     constexpr unsigned FULL = 0xffffffffu;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t s_bar[W * NS];
-    __shared__ float s_m[W][16], s_l[W][16];
+    __shared__ float s_m[W][16], s_l[W][16], s_qa[16];
     __shared__ int64_t s_sum[W], s_start;
     __shared__ int s_seq, s_last;
     __shared__ unsigned s_active;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const uint32_t ring = smem_u32(smem) + warp * Lay::kRing;
+    uint8_t *const ring = smem + warp * Lay::kRing;
     const uint32_t bars = smem_u32(s_bar) + warp * NS * 8;
     if (lane == 0) {
         for (int i = 0; i < NS; ++i) mbar_init(bars + 8 * i, 1);
@@ -133,11 +135,11 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     }
     if (tid == 0) s_seq = -1;
 
-    // ---- this worker's range of the stages, in (sequence, KV head, position) order
+    // ---- this worker's range of the weight, in (sequence, KV head, position) order
     const int per = (p.num_seqs + W * 32 - 1) / (W * 32);
     const int s_lo = min(tid * per, p.num_seqs), s_hi = min(s_lo + per, p.num_seqs);
     int64_t mine = 0;
-    for (int s = s_lo; s < s_hi; ++s) mine += int4_stages(int4_len(p, s, BS));
+    for (int s = s_lo; s < s_hi; ++s) mine += int4_weight(int4_len(p, s, BS));
     int64_t scan = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     if (range > 0 && lo >= before && lo < before + mine * p.num_kv_heads) {
         int64_t at = before;
         for (int s = s_lo; s < s_hi; ++s) {
-            const int64_t n = (int64_t)int4_stages(int4_len(p, s, BS)) * p.num_kv_heads;
+            const int64_t n = (int64_t)int4_weight(int4_len(p, s, BS)) * p.num_kv_heads;
             if (lo < at + n) {
                 s_seq = s;
                 s_start = at;
@@ -176,16 +178,18 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     Int4Seg seg = {};
     seg.s = s_seq;
     bool more = seg.s >= 0;
-    int64_t unit0 = 0;  // index of the current unit's first stage
+    int64_t unit0 = 0;  // where the current unit starts in the weight
     if (more) {
         seg.len = int4_len(p, seg.s, BS);
         seg.nt = int4_stages(seg.len);
-        seg.h = (int)((lo - s_start) / seg.nt);
-        seg.t0 = (int)(lo - s_start - (int64_t)seg.h * seg.nt);
-        seg.left = range;
-        seg.t1 = min(seg.nt, seg.t0 + range);
-        seg.pos = (unsigned)lo;
-        unit0 = lo - seg.t0;
+        const int weight = seg.nt + kI4UnitCost;
+        seg.h = (int)((lo - s_start) / weight);
+        unit0 = s_start + (int64_t)seg.h * weight;
+        const int off = (int)(lo - unit0);
+        seg.t0 = max(0, off - kI4UnitCost);
+        seg.t1 = min(seg.nt, off + range - kI4UnitCost);
+        seg.left = range - (weight - off);
+        more = seg.t0 < seg.t1;
     }
 
     // ---- the copies: this warp's next stage, its table entries fetched one stage ahead
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         __syncwarp();
         if (act) {
             const int64_t rec = ((int64_t)ent * p.num_kv_heads + ps.h) * REC;
-            bulk_load(ring + slot * Lay::kStage + ((lane & 1) * RECS + (lane >> 1)) * REC,
+            bulk_load(smem_u32(ring) + slot * Lay::kStage + ((lane & 1) * RECS + (lane >> 1)) * REC,
                       ((lane & 1) ? p.value_cache : p.key_cache) + rec, REC, bars + 8 * slot);
         }
         pt += W;
@@ -258,6 +262,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         // magnitude into [2^14, 2^15)), exact within 2^27 of that
         uint32_t qf[NG][KW][4];
         float qa[NG][2], qb[NG][2];
+        const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             const int head = n * 8 + g;
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 sum += __shfl_xor_sync(FULL, sum, off);
             }
             const int e = max((int)(top >> 23) - 127, -100);
-            const float mul = pow2i(max(14 - e, -126));
+            const float mul = pow2i(max(14 - e, -126)) * sign;
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
                 float x[8];
@@ -299,9 +304,11 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 qf[n][j][2] = pack_f16x2(x[2], x[6]);
                 qf[n][j][3] = pack_f16x2(x[3] * 0.0625f, x[7] * 0.0625f);
             }
-            // logit = (s S) qa + z qb; an infinity or a NaN in the query makes both NaN
-            float a = p.scale_log2 * 1024.f * pow2i(min(e, 127)), b = p.scale_log2 * sum;
-            if (top >= 0x7F800000u) a = b = __uint_as_float(0x7FC00000u);
+            // log2-logit = qa (s S + z qb): S = +-(q . codes) 2^-10 2^-e; an infinity or a NaN in the
+            // query makes it NaN.  qa > 0, so the largest product is the largest logit.
+            const float a = fminf(fmaxf(fabsf(p.scale_log2) * 1024.f * pow2i(min(e, 127)), 1.17549435e-38f), 3.4e38f);
+            const float b = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                                               : sum * (sign * 0.0009765625f) * pow2i(-(e >> 1)) * pow2i((e >> 1) - e);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 qa[n][i] = __shfl_sync(FULL, a, (2 * c + i) * 4);
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             }
         }
 
-        float o[NG][MT][4], m[NG][2], l[NG][2], zs[NG][2];
+        float o[NG][MT][4], m[NG][2], mlim[NG][2], l[NG][2], zs[NG][2];  // m, mlim: in units of qa
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
 #pragma unroll
@@ -318,12 +325,13 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m[n][i] = -INFINITY;
+                m[n][i] = mlim[n][i] = -INFINITY;
                 l[n][i] = zs[n][i] = 0.f;
             }
         }
         int ev = -1000;       // value scales of this unit are below 2^(ev + 1) so far
         float vmul = 0.f;     // 2^(10 - ev)
+        float vlim = 0.f;     // 2^(ev + 1)
         bool active = false;
         int freed = -1;       // the slot of this warp's last stage of the segment
         bool poison = false;
@@ -338,57 +346,59 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             }
             poison |= dead || ((badmask >> slot) & 1u);
             active = true;
-            const uint32_t kb = ring + slot * Lay::kStage, vb = kb + RECS * REC;
+            const uint8_t *kb = ring + slot * Lay::kStage, *vb = kb + RECS * REC;
 
             // ---- S = codes . q: 16 tokens x 8 heads x 16 dims a step
             float sc[2][NG][4];
+            uint32_t kw[2][2][KW];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const uint8_t *a = kb + row_at(2 * mt + hf, krow) + c * (D / 8);
+                    if constexpr (KW == 4) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(a);
+                        kw[mt][hf][0] = u.x, kw[mt][hf][1] = u.y, kw[mt][hf][2] = u.z, kw[mt][hf][3] = u.w;
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(a);
+                        kw[mt][hf][0] = u.x, kw[mt][hf][1] = u.y;
+                    }
+                }
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
-                uint32_t k0[KW], k1[KW];
-                const uint32_t a0 = kb + row_at(2 * mt, krow) + c * (D / 8);
-                const uint32_t a1 = kb + row_at(2 * mt + 1, krow) + c * (D / 8);
-                if constexpr (KW == 4) {
-                    const uint4 u = lds128(a0), v = lds128(a1);
-                    k0[0] = u.x, k0[1] = u.y, k0[2] = u.z, k0[3] = u.w;
-                    k1[0] = v.x, k1[1] = v.y, k1[2] = v.z, k1[3] = v.w;
-                } else {
-                    const uint2 u = lds64(a0), v = lds64(a1);
-                    k0[0] = u.x, k0[1] = u.y;
-                    k1[0] = v.x, k1[1] = v.y;
-                }
 #pragma unroll
-                for (int j = 0; j < KW; ++j) {
-                    const uint32_t u = k0[j], v = k1[j], u8 = u >> 8, v8 = v >> 8;
+            for (int j = 0; j < KW; ++j)
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    const uint32_t u = kw[mt][0][j], v = kw[mt][1][j], u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
                     for (int n = 0; n < NG; ++n) {
-                        mma_f16_16816(sc[mt][n], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
-                                      qf[n][j][0], qf[n][j][1]);
-                        mma_f16_16816(sc[mt][n], u8 & 0x000F000Fu, v8 & 0x000F000Fu, u8 & 0x00F000F0u,
-                                      v8 & 0x00F000F0u, qf[n][j][2], qf[n][j][3]);
+                        mma_codes(sc[mt][n], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
+                                  qf[n][j][0], qf[n][j][1]);
+                        mma_codes(sc[mt][n], u8 & 0x000F000Fu, v8 & 0x000F000Fu, u8 & 0x00F000F0u, v8 & 0x00F000F0u,
+                                  qf[n][j][2], qf[n][j][3]);
                     }
                 }
-            }
 
-            // ---- logits and the rows' pairs; row g + 8 * half of tile mt is token 8 (2 mt + half) + krow
+            // ---- logits / qa and the rows' pairs; row g + 8 * half of tile mt is token 8 (2 mt + half) + krow
             float2 vp[4];
-            const bool tail = (t + 1) * kI4Tokens > seg.len;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float2 kp = unpack_bf16x2(lds32(kb + pair_at(q, krow)));
-                vp[q] = unpack_bf16x2(lds32(vb + pair_at(q, krow)));
+                const float2 kp = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(kb + pair_at(q, krow)));
+                vp[q] = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(vb + pair_at(q, krow)));
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float &x = sc[q >> 1][n][(q & 1) * 2 + i];
-                        x = fmaf(kp.x * x, qa[n][i], kp.y * qb[n][i]);
+                        float &y = sc[q >> 1][n][(q & 1) * 2 + i];
+                        y = fmaf(kp.x, y, kp.y * qb[n][i]);
                     }
             }
-            if (tail) {
+            if ((t + 1) * kI4Tokens > seg.len) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     if (t * kI4Tokens + q * 8 + krow >= seg.len) {
@@ -400,34 +410,33 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
 
             // ---- running maximum and value scale, moved only when a logit passes the
             // maximum by more than 4 (so a weight stays below 2^4) or a scale its bound
-            bool move = false;
-            float vtop = 0.f;
+            const float vtop = fmaxf(fmaxf(vp[0].x, vp[1].x), fmaxf(vp[2].x, vp[3].x));
+            float top[NG][2];
+            bool move = vtop >= vlim;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                vtop = fmaxf(vtop, vp[q].x);
+            for (int n = 0; n < NG; ++n)
 #pragma unroll
-                for (int n = 0; n < NG; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) move |= sc[q >> 1][n][(q & 1) * 2 + i] > m[n][i] + 4.f;
-            }
-            const int ve = (int)(__float_as_uint(vtop) >> 23) - 127;
-            move |= ve > ev;
+                for (int i = 0; i < 2; ++i) {
+                    top[n][i] = fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]), fmaxf(sc[1][n][i], sc[1][n][2 + i]));
+                    move |= top[n][i] > mlim[n][i];
+                }
             if (__any_sync(FULL, move)) {
+                const int ve = (int)(__float_as_uint(vtop) >> 23) - 127;
                 const int en = max(max(ev, __reduce_max_sync(FULL, ve)), -100);
                 const float vcorr = exp2f((float)(ev - en));
                 ev = en;
                 vmul = pow2i(10 - en);
+                vlim = pow2i(min(en + 1, 127));
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float top = m[n][i];
+                        float to = fmaxf(m[n][i], top[n][i]);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) top = fmaxf(top, sc[q >> 1][n][(q & 1) * 2 + i]);
-#pragma unroll
-                        for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, off));
-                        const float corr = m[n][i] == -INFINITY ? 0.f : exp2f(m[n][i] - top);
-                        m[n][i] = top;
+                        for (int off = 4; off <= 16; off <<= 1) to = fmaxf(to, __shfl_xor_sync(FULL, to, off));
+                        const float corr = m[n][i] == -INFINITY ? 0.f : exp2f(qa[n][i] * (m[n][i] - to));
+                        m[n][i] = to;
+                        mlim[n][i] = to + 4.f / qa[n][i];
                         l[n][i] *= corr;  // a NaN stays one
                         zs[n][i] *= corr;
                         const float oc = corr * vcorr;
@@ -450,7 +459,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                     float w[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float pr = fast_exp2(sc[q >> 1][n][(q & 1) * 2 + i] - m[n][i]);
+                        const float pr = fast_exp2(qa[n][i] * (sc[q >> 1][n][(q & 1) * 2 + i] - m[n][i]));
                         l[n][i] += pr;
                         zs[n][i] = fmaf(pr, vp[q].y, zs[n][i]);
                         w[i] = pr * vs;
@@ -465,12 +474,12 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 uint32_t v[4][VW];  // tokens vrow0, vrow1 of group 2 mt, then of 2 mt + 1
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t a = vb + row_at(2 * mt + (i >> 1), (i & 1) ? vrow1 : vrow0) + g * (D / 16);
+                    const uint8_t *a = vb + row_at(2 * mt + (i >> 1), (i & 1) ? vrow1 : vrow0) + g * (D / 16);
                     if constexpr (VW == 2) {
-                        const uint2 u = lds64(a);
+                        const uint2 u = *reinterpret_cast<const uint2 *>(a);
                         v[i][0] = u.x, v[i][1] = u.y;
                     } else {
-                        v[i][0] = lds32(a);
+                        v[i][0] = *reinterpret_cast<const uint32_t *>(a);
                     }
                 }
 #pragma unroll
@@ -482,9 +491,9 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                         const uint32_t x8 = x >> 8, y8 = y >> 8;
 #pragma unroll
                         for (int n = 0; n < NG; ++n) {
-                            mma_f16_16816(o[n][4 * w + 2 * hw], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu,
+                            mma_codes(o[n][4 * w + 2 * hw], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu,
                                           y & 0x00F000F0u, pf[n][2 * mt], pf[n][2 * mt + 1]);
-                            mma_f16_16816(o[n][4 * w + 2 * hw + 1], x8 & 0x000F000Fu, x8 & 0x00F000F0u,
+                            mma_codes(o[n][4 * w + 2 * hw + 1], x8 & 0x000F000Fu, x8 & 0x00F000F0u,
                                           y8 & 0x000F000Fu, y8 & 0x00F000F0u, pf[n][2 * mt], pf[n][2 * mt + 1]);
                         }
                     }
@@ -511,8 +520,8 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         const bool whole = seg.t0 == 0 && seg.t1 == seg.nt;
         int first = me, last = me;
         if (!whole) {
-            first = seg.t0 == 0 ? me : int4_worker_of(unit0, quot, rest);
-            last = seg.t1 == seg.nt ? me : int4_worker_of(unit0 + seg.nt - 1, quot, rest);
+            first = seg.t0 == 0 ? me : int4_worker_of(unit0 + kI4UnitCost, quot, rest);
+            last = seg.t1 == seg.nt ? me : int4_worker_of(unit0 + kI4UnitCost + seg.nt - 1, quot, rest);
         }
         const int64_t part = 2 * (int64_t)me + (seg.t0 == 0 ? 1 : 0);
         if (tid == 0) s_active = 0;
@@ -532,6 +541,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                     if (g == 0) {
                         s_m[warp][n * 8 + 2 * c + i] = m[n][i];
                         s_l[warp][n * 8 + 2 * c + i] = l[n][i];
+                        s_qa[n * 8 + 2 * c + i] = qa[n][i];  // the same in every warp
                     }
                     const float f = pow2i(ev);  // out of the accumulators: 2^24 2^(ev - 10)
 #pragma unroll
@@ -540,10 +550,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                             fmaf(o[n][2 * k][i] * 16384.f, f, zs[n][i]), fmaf(o[n][2 * k][2 + i] * 1024.f, f, zs[n][i]),
                             fmaf(o[n][2 * k + 1][i] * 16384.f, f, zs[n][i]),
                             fmaf(o[n][2 * k + 1][2 + i] * 1024.f, f, zs[n][i]));
-                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         ring + freed * Lay::kStage + ((i * (MT / 2) + k) * 32 + lane) * 16),
-                                     "f"(r.x), "f"(r.y), "f"(r.z), "f"(r.w)
-                                     : "memory");
+                        *reinterpret_cast<float4 *>(ring + freed * Lay::kStage + ((i * (MT / 2) + k) * 32 + lane) * 16) = r;
                     }
                 }
             }
@@ -564,7 +571,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
 #pragma unroll
                 for (int w = 0; w < W; ++w)
                     if ((act >> w) & 1u) {
-                        const float f = exp2f(s_m[w][hd] - M);
+                        const float f = exp2f(s_qa[hd] * (s_m[w][hd] - M));
                         const float4 r = *reinterpret_cast<const float4 *>(smem + s_sum[w] + (k * 32 + lane) * 16);
                         L = fmaf(f, s_l[w][hd], L);
                         acc.x = fmaf(f, r.x, acc.x);
@@ -598,34 +605,86 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             __syncthreads();
             if (s_last) {
                 __threadfence();
+                // a thread per 4 dims of a head; where those are fewer than the threads, `ways` of
+                // them share the parts.  U parts are in flight at a time.
+                constexpr int U = 8;
+                const int items = p.group * (D / 4);
+                const int ways = items < W * 32 ? W * 32 / items : 1;
+                const int way = ways > 1 ? tid / items : 0;
+                uint8_t *const join = smem + s_sum[__ffs(s_active) - 1];  // a kept slot
+                for (int it = ways > 1 ? tid - way * items : tid; it < items && way < ways; it += W * 32) {
+                    const int hd = it / (D / 4), d4 = it % (D / 4);
+                    const int cell = (hd >> 3) * (Lay::kChunks * 32) +
+                                     ((hd & 1) * (D / 32) + d4 % (D / 32)) * 32 + d4 / (D / 32) * 4 + ((hd & 7) >> 1);
+                    const float fq = s_qa[hd];
+                    float M = -INFINITY, L = 0.f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int w = first + way; w <= last; w += ways * U) {
+                        float2 ml[U];
+                        float4 r[U];
 #pragma unroll
-                for (int n = 0; n < NG; ++n)
-                    for (int k = warp; k < Lay::kChunks; k += W) {
-                        const int hd = n * 8 + 2 * c + k / (Lay::kChunks / 2);
-                        const int dim = g * (D / 8) + 4 * (k % (Lay::kChunks / 2));
-                        if (hd >= p.group) continue;
+                        for (int u = 0; u < U; ++u) {
+                            const int x = w + u * ways;
+                            const int64_t q = 2 * x + (x == first ? 1 : 0);
+                            ml[u] = make_float2(-INFINITY, 0.f);
+                            r[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (x <= last) {
+                                ml[u] = __ldcg(&p.part_ml[q * 16 + hd]);
+                                r[u] = __ldcg(&p.part_o[q * (NG * Lay::kChunks * 32) + cell]);
+                            }
+                        }
+                        float to = M;
+#pragma unroll
+                        for (int u = 0; u < U; ++u) to = fmaxf(to, ml[u].x);
+                        const float corr = M == -INFINITY ? 0.f : exp2f(fq * (M - to));
+                        M = to;
+                        L *= corr;
+                        acc.x *= corr, acc.y *= corr, acc.z *= corr, acc.w *= corr;
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const float f = exp2f(fq * (ml[u].x - M));
+                            L = fmaf(f, ml[u].y, L);
+                            acc.x = fmaf(f, r[u].x, acc.x);
+                            acc.y = fmaf(f, r[u].y, acc.y);
+                            acc.z = fmaf(f, r[u].z, acc.z);
+                            acc.w = fmaf(f, r[u].w, acc.w);
+                        }
+                    }
+                    if (ways > 1) {
+                        *reinterpret_cast<float4 *>(join + tid * 16) = acc;
+                        if (d4 == 0) *reinterpret_cast<float2 *>(join + W * 32 * 16 + tid / (D / 4) * 8) = make_float2(M, L);
+                    } else {
+                        const float inv = 1.f / L;
+                        *reinterpret_cast<uint2 *>(
+                            p.out + ((int64_t)seg.s * p.num_heads + seg.h * p.group + hd) * D + 4 * d4) =
+                            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                    }
+                }
+                if (ways > 1) {
+                    __syncthreads();
+                    if (tid < items) {
+                        const int hd = tid / (D / 4);
+                        const float fq = s_qa[hd];
+                        const float2 *ml = reinterpret_cast<const float2 *>(join + W * 32 * 16);
                         float M = -INFINITY, L = 0.f;
                         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                        for (int w = first; w <= last; ++w)
-                            M = fmaxf(M, __ldcg(&p.part_ml[(2 * w + (w == first ? 1 : 0)) * 16 + hd]).x);
-#pragma unroll 8
-                        for (int w = first; w <= last; ++w) {
-                            const int64_t q = 2 * w + (w == first ? 1 : 0);
-                            const float2 ml = __ldcg(&p.part_ml[q * 16 + hd]);
-                            const float4 r = __ldcg(&p.part_o[(q * NG + n) * (Lay::kChunks * 32) + k * 32 + lane]);
-                            const float f = exp2f(ml.x - M);
-                            L = fmaf(f, ml.y, L);
+                        for (int y = 0; y < ways; ++y) M = fmaxf(M, ml[y * p.group + hd].x);
+                        for (int y = 0; y < ways; ++y) {
+                            const float2 v = ml[y * p.group + hd];
+                            const float4 r = *reinterpret_cast<const float4 *>(join + (y * items + tid) * 16);
+                            const float f = exp2f(fq * (v.x - M));
+                            L = fmaf(f, v.y, L);
                             acc.x = fmaf(f, r.x, acc.x);
                             acc.y = fmaf(f, r.y, acc.y);
                             acc.z = fmaf(f, r.z, acc.z);
                             acc.w = fmaf(f, r.w, acc.w);
                         }
                         const float inv = 1.f / L;
-                        *reinterpret_cast<uint2 *>(
-                            p.out + ((int64_t)seg.s * p.num_heads + seg.h * p.group + hd) * D + dim) =
+                        *reinterpret_cast<uint2 *>(p.out + ((int64_t)seg.s * p.num_heads + seg.h * p.group) * D + 4 * tid) =
                             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
                     }
+                    __syncthreads();
+                }
             }
         }
 
@@ -636,7 +695,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             issue(freed);
             ++issued;
         }
-        unit0 += seg.nt;
+        unit0 += seg.nt + kI4UnitCost;
         more = int4_next(seg, p, BS);
     }
     // a warp that gave up still waits, bounded, for the copies it has in flight
