@@ -12,7 +12,6 @@
 #pragma once
 
 #include "common.cuh"
-#include "decode.cuh"
 #include "row_ops.cuh"
 
 namespace pakv {
@@ -47,7 +46,7 @@ struct Int4Lay {
     static constexpr int kCtas = NG == 1 ? 4 : 3;              // resident CTAs per SM
     static_assert(kStage >= kChunks * 32 * 16, "a warp's result for 8 heads goes through one stage");
     static_assert(kStage >= kI4Warps * 32 * 16 + 8 * (kI4Warps * 32 / (D / 4)), "and a join of shared parts");
-    static_assert(kRec % 16 == 0 && kStage % 16 == 0, "bulk copies are multiples of 16 bytes");
+    static_assert(kRec % 16 == 0 && kStage % 16 == 0, "copies are 16 bytes wide");
 };
 
 // A unit (sequence, KV head) of nt stages weighs nt + kI4UnitCost stages when the
@@ -88,6 +87,18 @@ __device__ __forceinline__ bool int4_next(Int4Seg &g, const Int4DecodeParams &p,
     return true;
 }
 
+// 16 bytes global -> shared memory, asynchronous, past the L1.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // mma_f16_16816 without `volatile`: the compiler may interleave independent ones.
 __device__ __forceinline__ void mma_codes(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1)
@@ -119,7 +130,6 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     constexpr int MT = 4 * VW;    // 16-dim tiles of the output: a lane's 2 dims each
     constexpr unsigned FULL = 0xffffffffu;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t s_bar[W * NS];
     __shared__ float s_m[W][16], s_l[W][16], s_qa[16];
     __shared__ int64_t s_sum[W], s_start;
     __shared__ int s_seq, s_last;
@@ -128,11 +138,6 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     uint8_t *const ring = smem + warp * Lay::kRing;
-    const uint32_t bars = smem_u32(s_bar) + warp * NS * 8;
-    if (lane == 0) {
-        for (int i = 0; i < NS; ++i) mbar_init(bars + 8 * i, 1);
-        fence_mbarrier_init();
-    }
     if (tid == 0) s_seq = -1;
 
     // ---- this worker's range of the weight, in (sequence, KV head, position) order
@@ -202,37 +207,54 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             pvalid = int4_next(ps, p, BS);
             if (pvalid) pt = ps.t0 + ((warp - ps.pos) & (W - 1));
         }
-        if (pvalid && lane < 2 * RECS) {
-            const int i = pt * RECS + (lane >> 1);
+        if (pvalid && lane < RECS) {
+            const int i = pt * RECS + lane;
             if (i * BS < ps.len) ent = p.block_tables[(int64_t)ps.s * p.max_blocks + i];
         }
     };
+    const uint32_t ring32 = smem_u32(ring);
+    const uint32_t stride = (uint32_t)p.num_kv_heads * REC;
+    // One stage into a slot, 16 bytes a lane and copy: the codes of both caches, then the pairs.
     auto issue = [&](int slot) {
-        if (!pvalid) return;
-        const int recs = min(RECS, (ps.len - pt * kI4Tokens + BS - 1) / BS);
-        const bool act = lane < 2 * recs;
-        const bool bad = act && (ent < 0 || ent >= p.num_blocks);
-        if (bad) {
-            record_status(kStatusBadBlock);
-            ent = 0;  // block 0 stands in; the result becomes NaN
+        if (pvalid) {
+            const int recs = min(RECS, (ps.len - pt * kI4Tokens + BS - 1) / BS);
+            const bool bad = lane < recs && (uint32_t)ent >= (uint32_t)p.num_blocks;
+            badmask &= ~(1u << slot);
+            if (__any_sync(FULL, bad)) {
+                if (bad) {
+                    record_status(kStatusBadBlock);
+                    ent = 0;  // block 0 stands in; the result becomes NaN
+                }
+                badmask |= 1u << slot;
+            }
+            constexpr int CPR = BS * D / 32;  // 16-byte chunks of a record's codes
+            const uint32_t dst = ring32 + slot * Lay::kStage;
+            const int64_t head = (int64_t)ps.h * REC;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const int rec = (i * 32 + (CPR < 32 ? lane & ~(CPR - 1) : 0)) / CPR;
+                const int at = (CPR < 32 ? lane & (CPR - 1) : (i * 32) % CPR + lane) * 16;
+                const int64_t src = (uint64_t)(uint32_t)__shfl_sync(FULL, ent, rec) * stride + head + at;
+                if (rec < recs) {
+                    cp_async16(dst + rec * REC + at, p.key_cache + src);
+                    cp_async16(dst + (RECS + rec) * REC + at, p.value_cache + src);
+                }
+            }
+            constexpr int PPR = BS / 4;  // chunks of a record's pairs
+            const int rec = (lane & 7) / PPR, at = BS * (D / 2) + (lane & (PPR - 1)) * 16;
+            const int64_t src = (uint64_t)(uint32_t)__shfl_sync(FULL, ent, rec) * stride + head + at;
+            if (lane < 16 && rec < recs)
+                cp_async16(dst + ((lane >> 3) * RECS + rec) * REC + at, (lane < 8 ? p.key_cache : p.value_cache) + src);
+            pt += W;
+            settle();
         }
-        badmask = (badmask & ~(1u << slot)) | ((__ballot_sync(FULL, bad) != 0 ? 1u : 0u) << slot);
-        if (lane == 0) mbar_arrive_expect_tx(bars + 8 * slot, recs * 2 * REC);
-        __syncwarp();
-        if (act) {
-            const int64_t rec = ((int64_t)ent * p.num_kv_heads + ps.h) * REC;
-            bulk_load(smem_u32(ring) + slot * Lay::kStage + ((lane & 1) * RECS + (lane >> 1)) * REC,
-                      ((lane & 1) ? p.value_cache : p.key_cache) + rec, REC, bars + 8 * slot);
-        }
-        pt += W;
-        settle();
+        cp_async_commit();  // an empty group keeps the count where nothing is left
     };
     if (more) pt = seg.t0 + ((warp - seg.pos) & (W - 1));
     settle();
     pdl_wait();
     pdl_launch_dependents();
-    int issued = 0;
-    for (; issued < NS && pvalid; ++issued) issue(issued);
+    for (int i = 0; i < NS; ++i) issue(i);
 
     // rows of sequences without a token
     for (int s = me; s < p.num_seqs; s += gridDim.x)
@@ -254,9 +276,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                                               : BS == 16 ? (q >> 1) * REC + BS * RB + ((q & 1) * 8 + row) * 4
                                                          : BS * RB + (q * 8 + row) * 4; };
 
-    int arrived = 0, slot = 0;
-    uint32_t phase = 0;
-    bool dead = false;  // a wait gave up: nothing more is copied or waited for
+    int slot = 0;
     while (more) {
         // ---- the unit's queries: fp16, each head scaled by a power of two (its largest
         // magnitude into [2^14, 2^15)), exact within 2^27 of that
@@ -337,14 +357,9 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         bool poison = false;
 
         for (int t = seg.t0 + ((warp - seg.pos) & (W - 1)); t < seg.t1; t += W) {
-            if (!dead) {
-                dead = !__all_sync(FULL, mbar_wait_bounded(bars + 8 * slot, phase));
-                if (dead)
-                    record_timeout(kTimeoutFullBarrier);
-                else
-                    ++arrived;
-            }
-            poison |= dead || ((badmask >> slot) & 1u);
+            cp_async_wait<NS - 1>();
+            __syncwarp();
+            poison |= (badmask >> slot) & 1u;
             active = true;
             const uint8_t *kb = ring + slot * Lay::kStage, *vb = kb + RECS * REC;
 
@@ -502,17 +517,11 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             // ---- hand the slot back; the segment's last one first carries the result
             __syncwarp();
             if (t + W < seg.t1) {
-                if (!dead && pvalid) {
-                    issue(slot);
-                    ++issued;
-                }
+                issue(slot);
             } else {
                 freed = slot;
             }
-            if (++slot == NS) {
-                slot = 0;
-                phase ^= 1;
-            }
+            if (++slot == NS) slot = 0;
         }
 
         // ---- join the four warps: result of 8 heads at a time, [chunk][lane] float4s;
@@ -688,21 +697,12 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             }
         }
 
-        // ---- the kept slot can be filled again (its last readers and writers were generic)
-        if (freed >= 0 && !dead && pvalid) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            issue(freed);
-            ++issued;
-        }
+        // ---- the kept slot can be filled again
+        if (freed >= 0) issue(freed);
         unit0 += seg.nt + kI4UnitCost;
         more = int4_next(seg, p, BS);
     }
-    // a warp that gave up still waits, bounded, for the copies it has in flight
-    if (dead) {
-        for (int i = arrived; i < issued; ++i)
-            if (!mbar_wait_bounded(bars + 8 * (i % NS), (i / NS) & 1)) record_timeout(kTimeoutDrain);
-    }
+    cp_async_wait<0>();
 }
 
 }  // namespace pakv
