@@ -109,6 +109,19 @@ __device__ __forceinline__ void mma_codes(float *d, uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same without an addend.
+__device__ __forceinline__ void mma_codes_first(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// ev of vmul = 2^(10 - ev)
+__device__ __forceinline__ int int4_scale_exp(float vmul) { return 137 - (int)(__float_as_uint(vmul) >> 23); }
+
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 // The worker of position x when the weight is cut into ranges of q, the first r
@@ -131,7 +144,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     constexpr unsigned FULL = 0xffffffffu;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[W][16], s_l[W][16], s_qa[16];
-    __shared__ int64_t s_sum[W], s_start;
+    __shared__ int64_t s_sum[W], s_start, s_unit, s_quot, s_rest;
     __shared__ int s_seq, s_last;
     __shared__ unsigned s_active;
 
@@ -183,77 +196,106 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     Int4Seg seg = {};
     seg.s = s_seq;
     bool more = seg.s >= 0;
-    int64_t unit0 = 0;  // where the current unit starts in the weight
     if (more) {
         seg.len = int4_len(p, seg.s, BS);
         seg.nt = int4_stages(seg.len);
         const int weight = seg.nt + kI4UnitCost;
         seg.h = (int)((lo - s_start) / weight);
-        unit0 = s_start + (int64_t)seg.h * weight;
+        const int64_t unit0 = s_start + (int64_t)seg.h * weight;
         const int off = (int)(lo - unit0);
         seg.t0 = max(0, off - kI4UnitCost);
         seg.t1 = min(seg.nt, off + range - kI4UnitCost);
         seg.left = range - (weight - off);
         more = seg.t0 < seg.t1;
+        if (tid == 0) {
+            s_unit = unit0;  // where the current unit starts in the weight
+            s_quot = quot;
+            s_rest = rest;
+        }
     }
 
-    // ---- the copies: this warp's next stage, its table entries fetched one stage ahead
-    Int4Seg ps = seg;
-    int pt = 0, ent = 0;
-    bool pvalid = more;
-    unsigned badmask = 0;
-    auto settle = [&] {  // pt past its segment: on to the next one that has a stage for this warp
-        while (pvalid && pt >= ps.t1) {
-            pvalid = int4_next(ps, p, BS);
-            if (pvalid) pt = ps.t0 + ((warp - ps.pos) & (W - 1));
-        }
-        if (pvalid && lane < RECS) {
-            const int i = pt * RECS + lane;
-            if (i * BS < ps.len) ent = p.block_tables[(int64_t)ps.s * p.max_blocks + i];
-        }
-    };
+    // ---- the copies.  A lane holds one table entry of the batch of stages being copied (32 entries:
+    // 32 / RECS of this warp's stages of one unit) and one of the batch after it.
+    constexpr int CPR = BS * D / 32;  // 16-byte chunks of a record's codes
+    constexpr int PPR = BS / 4;       // and of its pairs
     const uint32_t ring32 = smem_u32(ring);
     const uint32_t stride = (uint32_t)p.num_kv_heads * REC;
+    const uint8_t *pk = nullptr, *pv = nullptr, *pp = nullptr;  // this lane's chunk of block 0's records
+    int pt = 0, pend = 0, pidx = 0, ent = 0;
+    Int4Seg ns = seg;  // the next batch: its unit, first stage and entries
+    bool nvalid = more;
+    int nstage = 0, nent = 0;
+    unsigned badmask = 0;
+    bool badbatch = false;
+    auto fetch = [&] {
+        while (nvalid && nstage >= ns.t1) {
+            nvalid = int4_next(ns, p, BS);
+            if (nvalid) nstage = ns.t0 + ((warp - ns.pos) & (W - 1));
+        }
+        if (nvalid) {  // past the end the last entry again: a stage is always copied whole
+            const int i = min((nstage + lane / RECS * W) * RECS + lane % RECS, (ns.len - 1) / BS);
+            nent = p.block_tables[(int64_t)ns.s * p.max_blocks + i];
+        }
+    };
+    auto take = [&] {
+        ent = nent;
+        pt = nstage;
+        pend = min(ns.t1, nstage + 32 / RECS * W);
+        pidx = 0;
+        const bool bad = (uint32_t)ent >= (uint32_t)p.num_blocks;
+        badbatch = __any_sync(FULL, bad);
+        if (bad) {
+            record_status(kStatusBadBlock);
+            ent = 0;  // block 0 stands in; the unit's result becomes NaN
+        }
+        const int64_t head = (int64_t)ns.h * REC;
+        pk = p.key_cache + head + (CPR < 32 ? lane & (CPR - 1) : lane) * 16;
+        pv = p.value_cache + head + (CPR < 32 ? lane & (CPR - 1) : lane) * 16;
+        pp = (lane < 8 ? p.key_cache : p.value_cache) + head + BS * (D / 2) + (lane & (PPR - 1)) * 16;
+        nstage += 32 / RECS * W;
+        fetch();
+    };
     // One stage into a slot, 16 bytes a lane and copy: the codes of both caches, then the pairs.
     auto issue = [&](int slot) {
-        if (pvalid) {
-            const int recs = min(RECS, (ps.len - pt * kI4Tokens + BS - 1) / BS);
-            const bool bad = lane < recs && (uint32_t)ent >= (uint32_t)p.num_blocks;
-            badmask &= ~(1u << slot);
-            if (__any_sync(FULL, bad)) {
-                if (bad) {
-                    record_status(kStatusBadBlock);
-                    ent = 0;  // block 0 stands in; the result becomes NaN
-                }
-                badmask |= 1u << slot;
-            }
-            constexpr int CPR = BS * D / 32;  // 16-byte chunks of a record's codes
+        if (pt < pend) {
+            badmask = (badmask & ~(1u << slot)) | ((badbatch ? 1u : 0u) << slot);
             const uint32_t dst = ring32 + slot * Lay::kStage;
-            const int64_t head = (int64_t)ps.h * REC;
+            if constexpr (CPR >= 32) {
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const int rec = (i * 32 + (CPR < 32 ? lane & ~(CPR - 1) : 0)) / CPR;
-                const int at = (CPR < 32 ? lane & (CPR - 1) : (i * 32) % CPR + lane) * 16;
-                const int64_t src = (uint64_t)(uint32_t)__shfl_sync(FULL, ent, rec) * stride + head + at;
-                if (rec < recs) {
-                    cp_async16(dst + rec * REC + at, p.key_cache + src);
-                    cp_async16(dst + (RECS + rec) * REC + at, p.value_cache + src);
+                for (int r = 0; r < RECS; ++r) {
+                    const uint64_t off = (uint64_t)(uint32_t)__shfl_sync(FULL, ent, pidx + r) * stride;
+#pragma unroll
+                    for (int i = 0; i < CPR / 32; ++i) {
+                        cp_async16(dst + r * REC + i * 512 + lane * 16, pk + off + i * 512);
+                        cp_async16(dst + (RECS + r) * REC + i * 512 + lane * 16, pv + off + i * 512);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < RECS / 2; ++i) {
+                    const int r = 2 * i + lane / CPR;
+                    const uint64_t off = (uint64_t)(uint32_t)__shfl_sync(FULL, ent, pidx + r) * stride;
+                    cp_async16(dst + r * REC + (lane & (CPR - 1)) * 16, pk + off);
+                    cp_async16(dst + (RECS + r) * REC + (lane & (CPR - 1)) * 16, pv + off);
                 }
             }
-            constexpr int PPR = BS / 4;  // chunks of a record's pairs
-            const int rec = (lane & 7) / PPR, at = BS * (D / 2) + (lane & (PPR - 1)) * 16;
-            const int64_t src = (uint64_t)(uint32_t)__shfl_sync(FULL, ent, rec) * stride + head + at;
-            if (lane < 16 && rec < recs)
-                cp_async16(dst + ((lane >> 3) * RECS + rec) * REC + at, (lane < 8 ? p.key_cache : p.value_cache) + src);
+            const int r = (lane & 7) / PPR;
+            const uint64_t off = (uint64_t)(uint32_t)__shfl_sync(FULL, ent, pidx + r) * stride;
+            if (lane < 16)
+                cp_async16(dst + ((lane >> 3) * RECS + r) * REC + BS * (D / 2) + (lane & (PPR - 1)) * 16, pp + off);
             pt += W;
-            settle();
+            pidx += RECS;
+            if (pt >= pend && nvalid) take();
         }
         cp_async_commit();  // an empty group keeps the count where nothing is left
     };
-    if (more) pt = seg.t0 + ((warp - seg.pos) & (W - 1));
-    settle();
+    if (more) {
+        nstage = seg.t0 + ((warp - seg.pos) & (W - 1));
+        fetch();
+    }
     pdl_wait();
     pdl_launch_dependents();
+    if (nvalid) take();
     for (int i = 0; i < NS; ++i) issue(i);
 
     // rows of sequences without a token
@@ -349,9 +391,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 l[n][i] = zs[n][i] = 0.f;
             }
         }
-        int ev = -1000;       // value scales of this unit are below 2^(ev + 1) so far
-        float vmul = 0.f;     // 2^(10 - ev)
-        float vlim = 0.f;     // 2^(ev + 1)
+        float vmul = 0.f;     // 2^(10 - ev): the unit's value scales are below 2^(ev + 1) so far (0: none yet)
         bool active = false;
         int freed = -1;       // the slot of this warp's last stage of the segment
         bool poison = false;
@@ -380,20 +420,18 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                     }
                 }
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int n = 0; n < NG; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
-#pragma unroll
             for (int j = 0; j < KW; ++j)
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     const uint32_t u = kw[mt][0][j], v = kw[mt][1][j], u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
                     for (int n = 0; n < NG; ++n) {
-                        mma_codes(sc[mt][n], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
-                                  qf[n][j][0], qf[n][j][1]);
+                        if (j == 0)
+                            mma_codes_first(sc[mt][n], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u,
+                                            v & 0x00F000F0u, qf[n][j][0], qf[n][j][1]);
+                        else
+                            mma_codes(sc[mt][n], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
+                                      qf[n][j][0], qf[n][j][1]);
                         mma_codes(sc[mt][n], u8 & 0x000F000Fu, v8 & 0x000F000Fu, u8 & 0x00F000F0u, v8 & 0x00F000F0u,
                                   qf[n][j][2], qf[n][j][3]);
                     }
@@ -427,7 +465,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             // maximum by more than 4 (so a weight stays below 2^4) or a scale its bound
             const float vtop = fmaxf(fmaxf(vp[0].x, vp[1].x), fmaxf(vp[2].x, vp[3].x));
             float top[NG][2];
-            bool move = vtop >= vlim;
+            bool move = vtop * vmul >= 2048.f;
 #pragma unroll
             for (int n = 0; n < NG; ++n)
 #pragma unroll
@@ -437,11 +475,10 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 }
             if (__any_sync(FULL, move)) {
                 const int ve = (int)(__float_as_uint(vtop) >> 23) - 127;
+                const int ev = vmul == 0.f ? -1000 : int4_scale_exp(vmul);
                 const int en = max(max(ev, __reduce_max_sync(FULL, ve)), -100);
                 const float vcorr = exp2f((float)(ev - en));
-                ev = en;
                 vmul = pow2i(10 - en);
-                vlim = pow2i(min(en + 1, 127));
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
 #pragma unroll
@@ -527,11 +564,6 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         // ---- join the four warps: result of 8 heads at a time, [chunk][lane] float4s;
         // chunk k of a lane: head 2c + k / (chunks / 2), dims g D/8 + 4 (k % (chunks / 2)) ..
         const bool whole = seg.t0 == 0 && seg.t1 == seg.nt;
-        int first = me, last = me;
-        if (!whole) {
-            first = seg.t0 == 0 ? me : int4_worker_of(unit0 + kI4UnitCost, quot, rest);
-            last = seg.t1 == seg.nt ? me : int4_worker_of(unit0 + kI4UnitCost + seg.nt - 1, quot, rest);
-        }
         const int64_t part = 2 * (int64_t)me + (seg.t0 == 0 ? 1 : 0);
         if (tid == 0) s_active = 0;
         __syncthreads();
@@ -552,7 +584,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                         s_l[warp][n * 8 + 2 * c + i] = l[n][i];
                         s_qa[n * 8 + 2 * c + i] = qa[n][i];  // the same in every warp
                     }
-                    const float f = pow2i(ev);  // out of the accumulators: 2^24 2^(ev - 10)
+                    const float f = pow2i(int4_scale_exp(vmul));  // out of the accumulators: 2^24 2^(ev - 10)
 #pragma unroll
                     for (int k = 0; k < MT / 2; ++k) {
                         const float4 r = make_float4(
@@ -603,6 +635,8 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
 
         // ---- a unit cut between workers: the last one to arrive joins its parts, in order
         if (!whole) {
+            const int first = seg.t0 == 0 ? me : int4_worker_of(s_unit + kI4UnitCost, s_quot, s_rest);
+            const int last = seg.t1 == seg.nt ? me : int4_worker_of(s_unit + kI4UnitCost + seg.nt - 1, s_quot, s_rest);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
@@ -699,7 +733,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
 
         // ---- the kept slot can be filled again
         if (freed >= 0) issue(freed);
-        unit0 += seg.nt + kI4UnitCost;
+        if (tid == 0) s_unit += seg.nt + kI4UnitCost;  // read behind the next join's barriers
         more = int4_next(seg, p, BS);
     }
     cp_async_wait<0>();
