@@ -4,14 +4,16 @@
 //     x_t = scale * (s_t (q . c_t) + z_t sum(q)),   p_t = 2^(x_t log2 e - m),
 //     out = (sum_t (p_t s'_t) c'_t + sum_t p_t z'_t) / sum_t p_t,
 // so a row's scale and zero meet its codes only in per-token scalars, and the
-// codes go to the tensor cores as they are: a nibble in bits 0-3 of a half word
-// is the fp16 subnormal c 2^-24, one in bits 4-7 is 16 c 2^-24, so one AND turns
-// a 32-bit word into two exact fp16 operands; the 16 goes into the query (key
-// product) or out of the accumulator (value product).
+// codes go to the tensor cores as they are.  Key product: a word's low nibbles, and
+// its high nibbles in place (16 c), are unsigned bytes after one AND each; the query
+// is an integer of 16 bits in two bytes.  Value product: a nibble in bits 0-3 of a
+// half word is the fp16 subnormal c 2^-24, one in bits 4-7 is 16 c 2^-24, so one AND
+// gives two exact operands, and the 16 comes out of the accumulator.
 // Included once, by pagedkv.cu.
 #pragma once
 
 #include "common.cuh"
+#include "decode.cuh"
 #include "row_ops.cuh"
 
 namespace pakv {
@@ -32,6 +34,7 @@ struct Int4DecodeParams {
     float4 *part_o;                     // [2 workers][NG * D/16 chunks][32 lanes]
     float scale_log2;                   // scale * log2(e)
     int num_seqs, num_heads, num_kv_heads, group, max_blocks, num_blocks, min_stages;
+    int c16, c256;                      // 16 and 256: from memory, so that they stay multiplications (another pipe)
 };
 
 template <int D, int BS, int NG>
@@ -39,11 +42,14 @@ struct Int4Lay {
     static constexpr int kRecs = kI4Tokens / BS;               // records of a stage, per cache
     static constexpr int kRec = BS * (D / 2 + 4);
     static constexpr int kStage = 2 * kRecs * kRec;            // K records, then V records
-    static constexpr int kSlots = D == 128 ? 3 : 5;            // stages in flight, per warp
+    static constexpr int kSlots = D == 128 ? 2 : 4;            // stages a warp holds
     static constexpr int kRing = kSlots * kStage;
     static constexpr int kChunks = D / 16;                     // float4s a lane holds of 8 heads
-    static constexpr int kBytes = kI4Warps * kRing;
     static constexpr int kCtas = NG == 1 ? 4 : 3;              // resident CTAs per SM
+    static constexpr int kQf = kI4Warps * kRing;               // the unit's queries as operands
+    static constexpr int kQraw = kQf + NG * (D / 32) * 512;    // and as they are, for this unit and the next
+    static constexpr int kQrawBytes = NG * 8 * D * 2;
+    static constexpr int kBytes = kQraw + 2 * kQrawBytes;
     static_assert(kStage >= kChunks * 32 * 16, "a warp's result for 8 heads goes through one stage");
     static_assert(kStage >= kI4Warps * 32 * 16 + 8 * (kI4Warps * 32 / (D / 4)), "and a join of shared parts");
     static_assert(kRec % 16 == 0 && kStage % 16 == 0, "copies are 16 bytes wide");
@@ -109,14 +115,22 @@ __device__ __forceinline__ void mma_codes(float *d, uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The same without an addend.
-__device__ __forceinline__ void mma_codes_first(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                uint32_t b0, uint32_t b1)
+// D = A(16x32, row, u8) * B(32x8, col) + C in s32; B unsigned, or signed where SGN; C = D, or 0 where ZERO.
+template <bool SGN, bool ZERO>
+__device__ __forceinline__ void mma_bytes(int *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    if constexpr (ZERO) d[0] = d[1] = d[2] = d[3] = 0;
+    if constexpr (SGN)
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]));
+    else
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]));
 }
 
 // ev of vmul = 2^(10 - ev)
@@ -143,7 +157,9 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     constexpr int MT = 4 * VW;    // 16-dim tiles of the output: a lane's 2 dims each
     constexpr unsigned FULL = 0xffffffffu;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_m[W][16], s_l[W][16], s_qa[16];
+    __shared__ float s_m[W][16], s_l[W][16], s_qa[16], s_qb[16];
+    __shared__ Int4Seg s_ns[W];
+    __shared__ __align__(8) uint64_t s_bar[2];
     __shared__ int64_t s_sum[W], s_start, s_unit, s_quot, s_rest;
     __shared__ int s_seq, s_last;
     __shared__ unsigned s_active;
@@ -151,7 +167,13 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     uint8_t *const ring = smem + warp * Lay::kRing;
-    if (tid == 0) s_seq = -1;
+    const uint32_t bars = smem_u32(s_bar), qraw32 = smem_u32(smem) + Lay::kQraw;
+    if (tid == 0) {
+        s_seq = -1;
+        mbar_init(bars, 1);
+        mbar_init(bars + 8, 1);
+        fence_mbarrier_init();
+    }
 
     // ---- this worker's range of the weight, in (sequence, KV head, position) order
     const int per = (p.num_seqs + W * 32 - 1) / (W * 32);
@@ -220,24 +242,25 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     constexpr int PPR = BS / 4;       // and of its pairs
     const uint32_t ring32 = smem_u32(ring);
     const uint32_t stride = (uint32_t)p.num_kv_heads * REC;
-    const uint8_t *pk = nullptr, *pv = nullptr, *pp = nullptr;  // this lane's chunk of block 0's records
-    int pt = 0, pend = 0, pidx = 0, ent = 0;
-    Int4Seg ns = seg;  // the next batch: its unit, first stage and entries
-    bool nvalid = more;
-    int nstage = 0, nent = 0;
-    unsigned badmask = 0;
-    bool badbatch = false;
-    auto fetch = [&] {
-        while (nvalid && nstage >= ns.t1) {
-            nvalid = int4_next(ns, p, BS);
-            if (nvalid) nstage = ns.t0 + ((warp - ns.pos) & (W - 1));
+    const uint8_t *pk = nullptr, *pv = nullptr;  // this lane's chunk of block 0's records
+    int pt = 0, pend = 0, pidx = 0, ent = 0, nent = 0, nstage = -1;  // nstage: the next batch's first (-1: none)
+    unsigned badmask = 0, badbatch = 0;
+    auto fetch = [&](Int4Seg &ns) {  // the next batch's unit, and its entries
+        while (nstage >= ns.t1) {
+            nstage = -1;
+            if (!int4_next(ns, p, BS)) break;
+            nstage = ns.t0 + ((warp - ns.pos) & (W - 1));
         }
-        if (nvalid) {  // past the end the last entry again: a stage is always copied whole
+        if (nstage >= 0) {  // past the end the last entry again: a stage is always copied whole
             const int i = min((nstage + lane / RECS * W) * RECS + lane % RECS, (ns.len - 1) / BS);
             nent = p.block_tables[(int64_t)ns.s * p.max_blocks + i];
         }
+        __syncwarp();
+        if (lane == 0) s_ns[warp] = ns;
+        __syncwarp();
     };
     auto take = [&] {
+        Int4Seg ns = s_ns[warp];
         ent = nent;
         pt = nstage;
         pend = min(ns.t1, nstage + 32 / RECS * W);
@@ -248,54 +271,60 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             record_status(kStatusBadBlock);
             ent = 0;  // block 0 stands in; the unit's result becomes NaN
         }
-        const int64_t head = (int64_t)ns.h * REC;
-        pk = p.key_cache + head + (CPR < 32 ? lane & (CPR - 1) : lane) * 16;
-        pv = p.value_cache + head + (CPR < 32 ? lane & (CPR - 1) : lane) * 16;
-        pp = (lane < 8 ? p.key_cache : p.value_cache) + head + BS * (D / 2) + (lane & (PPR - 1)) * 16;
+        const int64_t at = (int64_t)ns.h * REC + (CPR < 32 ? lane & (CPR - 1) : lane) * 16;
+        pk = p.key_cache + at;
+        pv = p.value_cache + at;
         nstage += 32 / RECS * W;
-        fetch();
+        fetch(ns);
     };
     // One stage into a slot, 16 bytes a lane and copy: the codes of both caches, then the pairs.
     auto issue = [&](int slot) {
         if (pt < pend) {
-            badmask = (badmask & ~(1u << slot)) | ((badbatch ? 1u : 0u) << slot);
+            badmask = (badmask & ~(1u << slot)) | (badbatch << slot);
+            const int chunk = CPR < 32 ? lane & (CPR - 1) : lane;
             const uint32_t dst = ring32 + slot * Lay::kStage;
-            if constexpr (CPR >= 32) {
+            // value rows are swizzled: chunk q of row r at q ^ r / 2 (r / 4)
+            const int vchunk = D == 128 ? chunk ^ ((chunk >> 3) & 3) : chunk ^ ((chunk >> 3) & 1);
 #pragma unroll
-                for (int r = 0; r < RECS; ++r) {
-                    const uint64_t off = (uint64_t)(uint32_t)__shfl_sync(FULL, ent, pidx + r) * stride;
+            for (int i = 0; i < (CPR < 32 ? RECS * CPR / 32 : RECS); ++i) {
+                const int r = CPR < 32 ? i * (32 / CPR) + lane / CPR : i;
+                const uint64_t off = (uint64_t)(uint32_t)__shfl_sync(FULL, ent, pidx + r) * stride;
+                const uint8_t *k = pk + off, *v = pv + off;
+                const uint32_t dk = dst + r * REC, dv = dk + RECS * REC;
 #pragma unroll
-                    for (int i = 0; i < CPR / 32; ++i) {
-                        cp_async16(dst + r * REC + i * 512 + lane * 16, pk + off + i * 512);
-                        cp_async16(dst + (RECS + r) * REC + i * 512 + lane * 16, pv + off + i * 512);
-                    }
+                for (int x = 0; x < (CPR + 31) / 32; ++x) {
+                    cp_async16(dk + chunk * 16 + x * 512, k + x * 512);
+                    cp_async16(dv + vchunk * 16 + x * 512, v + x * 512);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < RECS / 2; ++i) {
-                    const int r = 2 * i + lane / CPR;
-                    const uint64_t off = (uint64_t)(uint32_t)__shfl_sync(FULL, ent, pidx + r) * stride;
-                    cp_async16(dst + r * REC + (lane & (CPR - 1)) * 16, pk + off);
-                    cp_async16(dst + (RECS + r) * REC + (lane & (CPR - 1)) * 16, pv + off);
+                if (chunk < PPR) {
+                    cp_async16(dk + BS * (D / 2) + chunk * 16, k + BS * (D / 2));
+                    cp_async16(dv + BS * (D / 2) + chunk * 16, v + BS * (D / 2));
                 }
             }
-            const int r = (lane & 7) / PPR;
-            const uint64_t off = (uint64_t)(uint32_t)__shfl_sync(FULL, ent, pidx + r) * stride;
-            if (lane < 16)
-                cp_async16(dst + ((lane >> 3) * RECS + r) * REC + BS * (D / 2) + (lane & (PPR - 1)) * 16, pp + off);
             pt += W;
             pidx += RECS;
-            if (pt >= pend && nvalid) take();
+            if (pt >= pend && nstage >= 0) take();
         }
         cp_async_commit();  // an empty group keeps the count where nothing is left
     };
+    // a unit's queries into buffer b
+    auto fetch_q = [&](const Int4Seg &u, int b) {
+        if (tid == 0) {
+            const uint32_t bytes = p.group * D * 2;
+            mbar_arrive_expect_tx(bars + 8 * b, bytes);
+            bulk_load(qraw32 + b * Lay::kQrawBytes, p.query + ((int64_t)u.s * p.num_heads + u.h * p.group) * D, bytes,
+                      bars + 8 * b);
+        }
+    };
     if (more) {
         nstage = seg.t0 + ((warp - seg.pos) & (W - 1));
-        fetch();
+        Int4Seg ns = seg;
+        fetch(ns);
+        fetch_q(seg, 0);
     }
     pdl_wait();
     pdl_launch_dependents();
-    if (nvalid) take();
+    if (nstage >= 0) take();
     for (int i = 0; i < NS; ++i) issue(i);
 
     // rows of sequences without a token
@@ -305,10 +334,6 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             for (int i = tid; i < p.num_heads * D / 8; i += W * 32) row[i] = make_uint4(0u, 0u, 0u, 0u);
         }
 
-    // token of row r of an 8-token group: the order that spreads the value rows over the banks
-    constexpr uint32_t PERM = D == 128 ? 0x67542310u : 0x57463120u;
-    const int krow = (PERM >> (4 * g)) & 7;
-    const int vrow0 = (PERM >> (8 * c)) & 7, vrow1 = (PERM >> (8 * c + 4)) & 7;
     constexpr int RB = D / 2;  // bytes of a row
     // offset of token `row` (0..7) of 8-token group q (0..3) of a stage
     auto row_at = [&](int q, int row) { return BS == 8 ? q * REC + row * RB
@@ -318,34 +343,47 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                                               : BS == 16 ? (q >> 1) * REC + BS * RB + ((q & 1) * 8 + row) * 4
                                                          : BS * RB + (q * 8 + row) * 4; };
 
+    // this lane's row of the value tile's matrices: matrix lane / 8 is chunk 2 x2 + lane / 16, half
+    // (lane / 8) % 2; 16-byte chunk q of row r lies at q ^ r / 2 (D 128) or q ^ r / 4 (D 64), so that
+    // the 8 rows of a matrix fall in different banks
+    int vlane[VW];
+#pragma unroll
+    for (int x2 = 0; x2 < VW; ++x2) {
+        const int r = lane & 7, q = 2 * x2 + (lane >> 4);
+        vlane[x2] = row_at((lane >> 3) & 1, r) + (D == 128 ? q ^ (r >> 1) : q ^ (r >> 2)) * 16;
+    }
+
     int slot = 0;
-    while (more) {
-        // ---- the unit's queries: fp16, each head scaled by a power of two (its largest
-        // magnitude into [2^14, 2^15)), exact within 2^27 of that
-        uint32_t qf[NG][KW][4];
-        float qa[NG][2], qb[NG][2];
+    bool dead = false;  // a wait gave up: the results become NaN
+    unsigned waited = 0;
+    for (unsigned turn = 0; more; ++turn) {
+        // ---- the unit's queries: 16-bit integers, each head scaled by a power of two (its largest
+        // magnitude into [2^14, 2^15)): exact for entries within 2^8 of that, the others off by at most
+        // half a step.  Warp w packs the even (w even) or odd dims of words w & ~1, w | 1 of a row's lane.
+        if (!dead && !mbar_wait_bounded(bars + 8 * (turn & 1), (turn >> 1) & 1)) {
+            dead = true;
+            waited = turn;
+            record_timeout(kTimeoutFullBarrier);
+        }
+        Int4Seg nx = seg;
+        const bool more_next = int4_next(nx, p, BS);
         const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             const int head = n * 8 + g;
-            uint4 raw[KW];
-#pragma unroll
-            for (int j = 0; j < KW; ++j) {
-                raw[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (head < p.group)
-                    raw[j] = *reinterpret_cast<const uint4 *>(
-                        p.query + ((int64_t)seg.s * p.num_heads + seg.h * p.group + head) * D + c * (D / 4) + 8 * j);
-            }
+            const uint4 *raw = reinterpret_cast<const uint4 *>(smem + Lay::kQraw + (turn & 1) * Lay::kQrawBytes +
+                                                               (head * D + c * (D / 4)) * 2);
             uint32_t top = 0;
-            float sum = 0.f;
+            float sum = 0.f, x[8];
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
-                float x[8];
-                unpack8(raw[j], x);
+                float y[8];
+                unpack8(raw[j], y);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-                    sum += x[e];
+                    top = max(top, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+                    sum += y[e];
+                    if ((j >> 1) == (warp >> 1) && (e & 1) == (warp & 1)) x[(j & 1) * 4 + (e >> 1)] = y[e];
                 }
             }
 #pragma unroll
@@ -355,28 +393,39 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             }
             const int e = max((int)(top >> 23) - 127, -100);
             const float mul = pow2i(max(14 - e, -126)) * sign;
+            const bool live = head < p.group;  // the other columns are zero
+            if (warp < KW) {
+                uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
 #pragma unroll
-            for (int j = 0; j < KW; ++j) {
-                float x[8];
-                unpack8(raw[j], x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= mul;
-                qf[n][j][0] = pack_f16x2(x[0], x[4]);
-                qf[n][j][1] = pack_f16x2(x[1] * 0.0625f, x[5] * 0.0625f);
-                qf[n][j][2] = pack_f16x2(x[2], x[6]);
-                qf[n][j][3] = pack_f16x2(x[3] * 0.0625f, x[7] * 0.0625f);
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t v = live ? (uint32_t)__float2int_rn(x[i] * mul) : 0u;
+                    hi[i >> 2] |= ((v >> 8) & 255u) << (8 * (i & 3));
+                    lo[i >> 2] |= (v & 255u) << (8 * (i & 3));
+                }
+                *reinterpret_cast<uint4 *>(smem + Lay::kQf + ((n * KW + warp) * 32 + lane) * 16) =
+                    make_uint4(hi[0], hi[1], lo[0], lo[1]);
             }
-            // log2-logit = qa (s S + z qb): S = +-(q . codes) 2^-10 2^-e; an infinity or a NaN in the
+            // log2-logit = qa (s S + z qb): S = +-(q . codes) 2^18 2^-e; an infinity or a NaN in the
             // query makes it NaN.  qa > 0, so the largest product is the largest logit.
-            const float a = fminf(fmaxf(fabsf(p.scale_log2) * 1024.f * pow2i(min(e, 127)), 1.17549435e-38f), 3.4e38f);
-            const float b = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
-                                               : sum * (sign * 0.0009765625f) * pow2i(-(e >> 1)) * pow2i((e >> 1) - e);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                qa[n][i] = __shfl_sync(FULL, a, (2 * c + i) * 4);
-                qb[n][i] = __shfl_sync(FULL, b, (2 * c + i) * 4);
+            if (warp == 0 && c == 0) {
+                s_qa[head] = live ? fminf(fmaxf(fabsf(p.scale_log2) * 3.814697265625e-6f * pow2i(min(e, 127)), 1.17549435e-38f), 3.4e38f)
+                                  : 1.f;
+                s_qb[head] = !live ? 0.f
+                                   : top >= 0x7F800000u
+                                         ? __uint_as_float(0x7FC00000u)
+                                         : sum * (sign * 262144.f) * pow2i(-(e >> 1)) * pow2i((e >> 1) - e);
             }
         }
+        __syncthreads();
+        if (more_next && !dead) fetch_q(nx, (turn + 1) & 1);
+        float qa[NG][2], qb[NG][2];
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                qa[n][i] = s_qa[n * 8 + 2 * c + i];
+                qb[n][i] = s_qb[n * 8 + 2 * c + i];
+            }
 
         float o[NG][MT][4], m[NG][2], mlim[NG][2], l[NG][2], zs[NG][2];  // m, mlim: in units of qa
 #pragma unroll
@@ -394,7 +443,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         float vmul = 0.f;     // 2^(10 - ev): the unit's value scales are below 2^(ev + 1) so far (0: none yet)
         bool active = false;
         int freed = -1;       // the slot of this warp's last stage of the segment
-        bool poison = false;
+        bool poison = dead;
 
         for (int t = seg.t0 + ((warp - seg.pos) & (W - 1)); t < seg.t1; t += W) {
             cp_async_wait<NS - 1>();
@@ -402,47 +451,58 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             poison |= (badmask >> slot) & 1u;
             active = true;
             const uint8_t *kb = ring + slot * Lay::kStage, *vb = kb + RECS * REC;
+            const uint32_t vb32 = smem_u32(vb);
 
-            // ---- S = codes . q: 16 tokens x 8 heads x 16 dims a step
+            // ---- S = 16 codes . q: 16 tokens x 8 heads x 32 dims a step; the four sums (low or high
+            // nibbles) x (high or low byte of the query) are joined as integers below 2^31
             float sc[2][NG][4];
-            uint32_t kw[2][2][KW];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < 2; ++mt) {
+                uint32_t kw[2][KW];
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const uint8_t *a = kb + row_at(2 * mt + hf, krow) + c * (D / 8);
+                    const uint8_t *a = kb + row_at(2 * mt + hf, g) + c * (D / 8);
                     if constexpr (KW == 4) {
                         const uint4 u = *reinterpret_cast<const uint4 *>(a);
-                        kw[mt][hf][0] = u.x, kw[mt][hf][1] = u.y, kw[mt][hf][2] = u.z, kw[mt][hf][3] = u.w;
+                        kw[hf][0] = u.x, kw[hf][1] = u.y, kw[hf][2] = u.z, kw[hf][3] = u.w;
                     } else {
                         const uint2 u = *reinterpret_cast<const uint2 *>(a);
-                        kw[mt][hf][0] = u.x, kw[mt][hf][1] = u.y;
+                        kw[hf][0] = u.x, kw[hf][1] = u.y;
                     }
                 }
 #pragma unroll
-            for (int j = 0; j < KW; ++j)
+                for (int n = 0; n < NG; ++n) {
+                    int s4[2][2][4];  // [nibble][byte]
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    const uint32_t u = kw[mt][0][j], v = kw[mt][1][j], u8 = u >> 8, v8 = v >> 8;
+                    for (int j = 0; j < KW; j += 2)
 #pragma unroll
-                    for (int n = 0; n < NG; ++n) {
-                        if (j == 0)
-                            mma_codes_first(sc[mt][n], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u,
-                                            v & 0x00F000F0u, qf[n][j][0], qf[n][j][1]);
-                        else
-                            mma_codes(sc[mt][n], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
-                                      qf[n][j][0], qf[n][j][1]);
-                        mma_codes(sc[mt][n], u8 & 0x000F000Fu, v8 & 0x000F000Fu, u8 & 0x00F000F0u, v8 & 0x00F000F0u,
-                                  qf[n][j][2], qf[n][j][3]);
-                    }
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t mask = h ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
+                            const uint4 qf = *reinterpret_cast<const uint4 *>(smem + Lay::kQf +
+                                                                              ((n * KW + j + h) * 32 + lane) * 16);
+                            const uint32_t a0 = kw[0][j] & mask, a1 = kw[1][j] & mask, a2 = kw[0][j + 1] & mask,
+                                           a3 = kw[1][j + 1] & mask;
+                            if (j == 0) {
+                                mma_bytes<true, true>(s4[h][0], a0, a1, a2, a3, qf.x, qf.y);
+                                mma_bytes<false, true>(s4[h][1], a0, a1, a2, a3, qf.z, qf.w);
+                            } else {
+                                mma_bytes<true, false>(s4[h][0], a0, a1, a2, a3, qf.x, qf.y);
+                                mma_bytes<false, false>(s4[h][1], a0, a1, a2, a3, qf.z, qf.w);
+                            }
+                        }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sc[mt][n][e] = __int2float_rn((s4[0][0][e] * p.c16 + s4[1][0][e]) * p.c256 +
+                                                      (s4[0][1][e] * p.c16 + s4[1][1][e]));
                 }
+            }
 
-            // ---- logits / qa and the rows' pairs; row g + 8 * half of tile mt is token 8 (2 mt + half) + krow
+            // ---- logits / qa and the rows' pairs; row g + 8 half of tile mt is token 8 (2 mt + half) + g
             float2 vp[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float2 kp = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(kb + pair_at(q, krow)));
-                vp[q] = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(vb + pair_at(q, krow)));
+                const float2 kp = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(kb + pair_at(q, g)));
+                vp[q] = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(vb + pair_at(q, g)));
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
 #pragma unroll
@@ -454,7 +514,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             if ((t + 1) * kI4Tokens > seg.len) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (t * kI4Tokens + q * 8 + krow >= seg.len) {
+                    if (t * kI4Tokens + q * 8 + g >= seg.len) {
                         vp[q] = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int n = 0; n < NG; ++n) sc[q >> 1][n][(q & 1) * 2] = sc[q >> 1][n][(q & 1) * 2 + 1] = -INFINITY;
@@ -523,32 +583,23 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             // ---- O += codes' . w: 16 dims x 8 heads x 16 tokens a step
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-                uint32_t v[4][VW];  // tokens vrow0, vrow1 of group 2 mt, then of 2 mt + 1
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint8_t *a = vb + row_at(2 * mt + (i >> 1), (i & 1) ? vrow1 : vrow0) + g * (D / 16);
-                    if constexpr (VW == 2) {
-                        const uint2 u = *reinterpret_cast<const uint2 *>(a);
-                        v[i][0] = u.x, v[i][1] = u.y;
-                    } else {
-                        v[i][0] = *reinterpret_cast<const uint32_t *>(a);
-                    }
-                }
-#pragma unroll
-                for (int w = 0; w < VW; ++w)
+                for (int x2 = 0; x2 < VW; ++x2) {
+                    // [chunk][half] of 8 tokens x 8 half words: a lane gets half word g of tokens 2c, 2c + 1
+                    uint32_t v[2][2];
+                    ldsm_x4_trans(vb32 + row_at(2 * mt, 0) + vlane[x2], v[0][0], v[0][1], v[1][0], v[1][1]);
 #pragma unroll
                     for (int hw = 0; hw < 2; ++hw) {
-                        const uint32_t sel = hw ? 0x7632u : 0x5410u;
-                        const uint32_t x = prmt(v[0][w], v[1][w], sel), y = prmt(v[2][w], v[3][w], sel);
-                        const uint32_t x8 = x >> 8, y8 = y >> 8;
+                        const uint32_t x = v[hw][0], y = v[hw][1], x8 = x >> 8, y8 = y >> 8;
 #pragma unroll
                         for (int n = 0; n < NG; ++n) {
-                            mma_codes(o[n][4 * w + 2 * hw], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu,
-                                          y & 0x00F000F0u, pf[n][2 * mt], pf[n][2 * mt + 1]);
-                            mma_codes(o[n][4 * w + 2 * hw + 1], x8 & 0x000F000Fu, x8 & 0x00F000F0u,
-                                          y8 & 0x000F000Fu, y8 & 0x00F000F0u, pf[n][2 * mt], pf[n][2 * mt + 1]);
+                            mma_codes(o[n][4 * x2 + 2 * hw], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu,
+                                      y & 0x00F000F0u, pf[n][2 * mt], pf[n][2 * mt + 1]);
+                            mma_codes(o[n][4 * x2 + 2 * hw + 1], x8 & 0x000F000Fu, x8 & 0x00F000F0u, y8 & 0x000F000Fu,
+                                      y8 & 0x00F000F0u, pf[n][2 * mt], pf[n][2 * mt + 1]);
                         }
                     }
+                }
             }
 
             // ---- hand the slot back; the segment's last one first carries the result
@@ -562,7 +613,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         }
 
         // ---- join the four warps: result of 8 heads at a time, [chunk][lane] float4s;
-        // chunk k of a lane: head 2c + k / (chunks / 2), dims g D/8 + 4 (k % (chunks / 2)) ..
+        // chunk k of a lane: head 2c + k / (chunks / 2), dims 32 (k % (chunks / 2)) + 4 g ..
         const bool whole = seg.t0 == 0 && seg.t1 == seg.nt;
         const int64_t part = 2 * (int64_t)me + (seg.t0 == 0 ? 1 : 0);
         if (tid == 0) s_active = 0;
@@ -582,7 +633,6 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                     if (g == 0) {
                         s_m[warp][n * 8 + 2 * c + i] = m[n][i];
                         s_l[warp][n * 8 + 2 * c + i] = l[n][i];
-                        s_qa[n * 8 + 2 * c + i] = qa[n][i];  // the same in every warp
                     }
                     const float f = pow2i(int4_scale_exp(vmul));  // out of the accumulators: 2^24 2^(ev - 10)
 #pragma unroll
@@ -602,7 +652,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
 #pragma unroll
             for (int k = warp; k < Lay::kChunks; k += W) {
                 const int hd = n * 8 + 2 * c + k / (Lay::kChunks / 2);
-                const int dim = g * (D / 8) + 4 * (k % (Lay::kChunks / 2));
+                const int dim = 32 * (k % (Lay::kChunks / 2)) + 4 * g;
                 if (hd >= p.group) continue;
                 float M = -INFINITY, L = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -658,7 +708,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 for (int it = ways > 1 ? tid - way * items : tid; it < items && way < ways; it += W * 32) {
                     const int hd = it / (D / 4), d4 = it % (D / 4);
                     const int cell = (hd >> 3) * (Lay::kChunks * 32) +
-                                     ((hd & 1) * (D / 32) + d4 % (D / 32)) * 32 + d4 / (D / 32) * 4 + ((hd & 7) >> 1);
+                                     ((hd & 1) * (D / 32) + d4 / 8) * 32 + d4 % 8 * 4 + ((hd & 7) >> 1);
                     const float fq = s_qa[hd];
                     float M = -INFINITY, L = 0.f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -734,9 +784,12 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         // ---- the kept slot can be filled again
         if (freed >= 0) issue(freed);
         if (tid == 0) s_unit += seg.nt + kI4UnitCost;  // read behind the next join's barriers
-        more = int4_next(seg, p, BS);
+        seg = nx;
+        more = more_next;
     }
     cp_async_wait<0>();
+    // a wait for the queries that gave up: the copy may still be on its way (one more bounded wait)
+    if (dead && !mbar_wait_bounded(bars + 8 * (waited & 1), (waited >> 1) & 1)) record_timeout(kTimeoutDrain);
 }
 
 }  // namespace pakv

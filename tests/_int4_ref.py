@@ -78,6 +78,8 @@ def decode(query, key_cache, value_cache, tables, lens, scale, block_size):
         15 s'_t, averaged with weights p_t / l),
       * fp32 logits: (D + 8) roundings of the sum of |q| (|z| + 15 s), which move a weight by that much
         relative, twice (numerator and denominator),
+      * the query as 16-bit integers: multiples of 2^(e - 14) where 2^e is the binade of the head's largest
+        entry; what an entry is off by counts with 15 s, twice,
       * fp32 sums over L tokens and the exponential's 2^-22."""
     B, Hq, D = query.shape
     k, v = values(key_cache, block_size, D), values(value_cache, block_size, D)
@@ -101,7 +103,10 @@ def decode(query, key_cache, value_cache, tables, lens, scale, block_size):
         o = torch.einsum("hgt,thd->hgd", p, vv)
         out[i] = o.reshape(Hq, D)
         mag = (q.abs().sum(-1, keepdim=True) * sk.t()[:, None] * abs(scale)).amax(-1)        # [H, G]
-        rel = 2 * (D + 8) * half_step(F32) * mag + (L + 16) * half_step(F32) + 2.0 ** -21
+        step = torch.exp2(torch.floor(torch.log2(q.abs().amax(-1, keepdim=True).clamp(min=2.0 ** -100))) - 14)
+        off = (q - torch.round(q / step) * step).abs().sum(-1)                               # [H, G]
+        off = off * (ks[ids].reshape(-1, H)[:L].abs().amax(0) * 15)[:, None] * abs(scale)
+        rel = 2 * (D + 8) * half_step(F32) * mag + 2 * off + (L + 16) * half_step(F32) + 2.0 ** -21
         span = (vv.amax((0, 2)) - vv.amin((0, 2))).abs() + vv.abs().amax((0, 2))             # [H]
         wq = half_step(torch.float16) * torch.einsum("hgt,th->hg", p, sv)
         b = (wq + rel * span[:, None])[..., None] + half_step(torch.bfloat16) * 1.01 * o.abs()
