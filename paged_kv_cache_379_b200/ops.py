@@ -381,31 +381,75 @@ def decode_shared(query, key_cache, value_cache, block_tables, seq_lens, scale: 
 
 # ---- 4-bit cache ----------------------------------------------------------------------
 
-def _on_current(*tensors) -> None:
-    """The library launches on the current device: every tensor has to live there."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != cur:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+# The calls below are made once per layer and step, where the time of the marshalling itself counts: they ask
+# each tensor for as little as the checks need (get_device, dim and size answer without building objects).
 
-
-def _rows(t, name: str, heads: int | None = None, head_dim: int | None = None, tokens: int | None = None):
-    """(pointer, token stride) of a bf16 [tokens, heads, head_dim] view whose rows are contiguous."""
+def _device(t, name: str) -> int:
+    """The device of a call's first tensor: the library launches on the current one, so it has to be that."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
-    want = tuple(w if w is not None else n for w, n in zip((tokens, heads, head_dim), t.shape))
-    if tuple(t.shape) != want:
-        raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
-    row = t.shape[1] * t.shape[2]
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _on(dev: int, t, name: str) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    d = t.get_device()
+    if d != dev:
+        raise ValueError(f"{name} must be a CUDA tensor" if d < 0 else f"{name} is on cuda:{d}, not on cuda:{dev}")
+
+
+def _arr(dev: int, t, dtype, name: str, ndim: int, n: int = -1):
+    """Pointer of a contiguous tensor of a type and rank (and length, where n >= 0) on the call's device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        shape = t.shape
+        if len(shape) == ndim and (n < 0 or shape[0] == n):
+            return t.data_ptr()
+    _on(dev, t, name)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have {n} entries, got {t.size(0)}")
+
+
+def _opt(dev: int, t, dtype, name: str, n: int):
+    return None if t is None else _arr(dev, t, dtype, name, 1, n)
+
+
+def _rows(dev: int, t, name: str, tokens: int, heads: int, head_dim: int):
+    """(pointer, token stride) of a bf16 [tokens, heads, head_dim] view whose rows are contiguous."""
+    _on(dev, t, name)
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.shape != (tokens, heads, head_dim):
+        raise ValueError(f"{name} must be {[tokens, heads, head_dim]}, got {list(t.shape)}")
+    st = t.stride()
+    if tokens and (st[2] != 1 or (heads > 1 and st[1] != head_dim)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else row)
+    return t.data_ptr(), (st[0] if tokens > 1 else heads * head_dim)
+
+
+def _dims3(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have 3 dims, got {tuple(shape)}")
+    return shape
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)  # current_stream(dev).cuda_stream without the objects
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def int4_record_bytes(block_size: int, head_dim: int) -> int:
@@ -419,72 +463,64 @@ def new_int4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim
                        device=device)
 
 
-def _int4_dims(key_cache, value_cache, head_dim: int):
-    _dev(key_cache, torch.uint8, "key_cache", 3)
-    _dev(value_cache, torch.uint8, "value_cache", 3)
-    if key_cache.shape != value_cache.shape:
-        raise ValueError("key_cache and value_cache shapes differ")
+def _int4_caches(dev: int, key_cache, value_cache, head_dim: int):
+    """(key pointer, value pointer, num_blocks, block_size, num_kv_heads) of two 4-bit caches."""
+    kc = _arr(dev, key_cache, torch.uint8, "key_cache", 3)
+    vc = _arr(dev, value_cache, torch.uint8, "value_cache", 3)
     nb, hkv, rec = key_cache.shape
-    if head_dim <= 0 or rec % (head_dim // 2 + 4) != 0:
+    if value_cache.shape != key_cache.shape:
+        raise ValueError("key_cache and value_cache shapes differ")
+    row = head_dim // 2 + 4
+    if head_dim <= 0 or rec % row != 0:
         raise ValueError(f"cache records of {rec} bytes do not hold rows of head_dim {head_dim}")
-    return nb, rec // (head_dim // 2 + 4), hkv
+    return kc, vc, nb, rec // row, hkv
 
 
 def reshape_and_cache_int4(key, value, key_cache, value_cache, slot_mapping, stream=None) -> None:
     """pa_reshape_and_cache_int4: bf16 rows (strided by token) quantised into 4-bit caches."""
-    k, ks = _rows(key, "key")
-    T, hkv, d = key.shape
-    nb, bs, heads = _int4_dims(key_cache, value_cache, d)
-    v, vs = _rows(value, "value", heads, d, T)
-    if hkv != heads:
-        raise ValueError("key/value must be [num_tokens, num_kv_heads, head_dim] matching the cache")
-    sm = _dev(slot_mapping, torch.int64, "slot_mapping", 1)
-    if slot_mapping.shape[0] != T:
-        raise ValueError("slot_mapping length != num_tokens")
-    _on_current(key, value, key_cache, value_cache, slot_mapping)
+    dev = _device(key, "key")
+    T, _, d = _dims3(key, "key")
+    kc, vc, nb, bs, hkv = _int4_caches(dev, key_cache, value_cache, d)
+    k, ks = _rows(dev, key, "key", T, hkv, d)
+    v, vs = _rows(dev, value, "value", T, hkv, d)
+    sm = _arr(dev, slot_mapping, torch.int64, "slot_mapping", 1, T)
     check("pa_reshape_and_cache_int4", load().pa_reshape_and_cache_int4(
-        k, v, ks, vs, key_cache.data_ptr(), value_cache.data_ptr(), sm, T, hkv, d, bs, nb, _stream(stream)))
+        k, v, ks, vs, kc, vc, sm, T, hkv, d, bs, nb, _raw_stream(stream, dev)))
 
 
 def append_decode_kv_int4(key, value, key_cache, value_cache, block_tables, seq_lens, slot_mapping=None,
                           stream=None) -> None:
     """pa_append_decode_kv_int4: as append_decode_kv into 4-bit caches."""
-    B = seq_lens.shape[0]
-    k, ks = _rows(key, "key", tokens=B)
-    _, hkv, d = key.shape
-    nb, bs, heads = _int4_dims(key_cache, value_cache, d)
-    v, vs = _rows(value, "value", heads, d, B)
-    if hkv != heads:
-        raise ValueError("key/value must be [num_seqs, num_kv_heads, head_dim] matching the cache")
-    bt = _dev(block_tables, torch.int32, "block_tables", 2)
-    if block_tables.shape[0] != B:
-        raise ValueError("block_tables rows != num_seqs")
-    sm = _dev(slot_mapping, torch.int64, "slot_mapping", 1)
-    if slot_mapping is not None and slot_mapping.shape[0] != B:
-        raise ValueError("slot_mapping length != num_seqs")
-    _on_current(key, value, key_cache, value_cache, block_tables, seq_lens, slot_mapping)
+    dev = _device(key, "key")
+    B, _, d = _dims3(key, "key")
+    kc, vc, nb, bs, hkv = _int4_caches(dev, key_cache, value_cache, d)
+    k, ks = _rows(dev, key, "key", B, hkv, d)
+    v, vs = _rows(dev, value, "value", B, hkv, d)
+    bt = _arr(dev, block_tables, torch.int32, "block_tables", 2, B)
+    sl = _arr(dev, seq_lens, torch.int32, "seq_lens", 1, B)
+    sm = _opt(dev, slot_mapping, torch.int64, "slot_mapping", B)
     check("pa_append_decode_kv_int4", load().pa_append_decode_kv_int4(
-        k, v, ks, vs, key_cache.data_ptr(), value_cache.data_ptr(), bt, _dev(seq_lens, torch.int32, "seq_lens", 1),
-        sm, B, block_tables.shape[1], hkv, d, bs, nb, _stream(stream)))
+        k, v, ks, vs, kc, vc, bt, sl, sm, B, block_tables.size(1), hkv, d, bs, nb, _raw_stream(stream, dev)))
 
 
 def dequantize_blocks_int4(key_cache, value_cache, block_ids, head_dim: int, *, key_out=None, value_out=None,
                            stream=None):
     """pa_dequantize_blocks_int4: the listed blocks as bf16 blocks [n, block_size, num_kv_heads, head_dim]."""
-    nb, bs, hkv = _int4_dims(key_cache, value_cache, head_dim)
-    ids = _dev(block_ids, torch.int32, "block_ids", 1)
-    shape = (block_ids.shape[0], bs, hkv, int(head_dim))
+    dev, d = _device(key_cache, "key_cache"), int(head_dim)
+    kc, vc, nb, bs, hkv = _int4_caches(dev, key_cache, value_cache, d)
+    ids = _arr(dev, block_ids, torch.int32, "block_ids", 1)
+    n = block_ids.size(0)
     if key_out is None:
-        key_out = torch.zeros(shape, dtype=torch.bfloat16, device=key_cache.device)
+        key_out = torch.zeros((n, bs, hkv, d), dtype=torch.bfloat16, device=key_cache.device)
     if value_out is None:
-        value_out = torch.zeros(shape, dtype=torch.bfloat16, device=key_cache.device)
-    ko, vo = _dev(key_out, torch.bfloat16, "key_out", 4), _dev(value_out, torch.bfloat16, "value_out", 4)
-    if tuple(key_out.shape) != shape or tuple(value_out.shape) != shape:
+        value_out = torch.zeros((n, bs, hkv, d), dtype=torch.bfloat16, device=key_cache.device)
+    ko = _arr(dev, key_out, torch.bfloat16, "key_out", 4, n)
+    vo = _arr(dev, value_out, torch.bfloat16, "value_out", 4, n)
+    shape = (n, bs, hkv, d)
+    if key_out.shape != shape or value_out.shape != shape:
         raise ValueError(f"key_out / value_out must be {list(shape)}")
-    _on_current(key_cache, value_cache, block_ids, key_out, value_out)
     check("pa_dequantize_blocks_int4", load().pa_dequantize_blocks_int4(
-        ko, vo, key_cache.data_ptr(), value_cache.data_ptr(), ids, shape[0], hkv, int(head_dim), bs, nb,
-        _stream(stream)))
+        ko, vo, kc, vc, ids, n, hkv, d, bs, nb, _raw_stream(stream, dev)))
     return key_out, value_out
 
 
@@ -502,80 +538,83 @@ def new_int4_workspace(num_heads: int, num_kv_heads: int, head_dim: int, device=
 def decode_int4(query, key_cache, value_cache, block_tables, seq_lens, scale: float, workspace, *, out=None,
                 stream=None):
     """pa_decode_int4: single-query paged decode over 4-bit caches."""
-    q = _dev(query, torch.bfloat16, "query", 3)
-    B, hq, d = query.shape
-    nb, bs, hkv = _int4_dims(key_cache, value_cache, d)
-    bt = _dev(block_tables, torch.int32, "block_tables", 2)
-    sl = _dev(seq_lens, torch.int32, "seq_lens", 1)
-    if block_tables.shape[0] != B or seq_lens.shape[0] != B:
-        raise ValueError("block_tables / seq_lens batch size != query batch size")
-    o, out = _out(out, query)
+    dev = _device(query, "query")
+    B, hq, d = _dims3(query, "query")
+    q = _arr(dev, query, torch.bfloat16, "query", 3)
+    kc, vc, nb, bs, hkv = _int4_caches(dev, key_cache, value_cache, d)
+    bt = _arr(dev, block_tables, torch.int32, "block_tables", 2, B)
+    sl = _arr(dev, seq_lens, torch.int32, "seq_lens", 1, B)
+    if out is None:
+        out = torch.empty_like(query)
+    o = _arr(dev, out, torch.bfloat16, "out", 3, B)
     if out.shape != query.shape:
         raise ValueError("out must have the query's shape")
-    wp, wb = _ws(workspace)
-    _on_current(query, key_cache, value_cache, block_tables, seq_lens, out, workspace)
+    if workspace is None:
+        wp, wb = None, 0
+    else:
+        _on(dev, workspace, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        wp, wb = workspace.data_ptr(), workspace.nbytes
     check("pa_decode_int4", load().pa_decode_int4(
-        o, q, key_cache.data_ptr(), value_cache.data_ptr(), bt, sl, float(scale), bs, hkv, B, hq, d,
-        block_tables.shape[1], nb, wp, wb, _stream(stream)))
+        o, q, kc, vc, bt, sl, float(scale), bs, hkv, B, hq, d, block_tables.size(1), nb, wp, wb,
+        _raw_stream(stream, dev)))
     return out
 
 
 # ---- head norm + rotation -------------------------------------------------------------
 
 def _rope_args(query, key, q_weight, k_weight, cos_sin, positions, query_out):
-    q, qs = _rows(query, "query")
-    T, hq, d = query.shape
-    k, ks = _rows(key, "key", head_dim=d, tokens=T)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _dev(w, torch.bfloat16, name, 1)
-        if w is not None and w.shape[0] != d:
-            raise ValueError(f"{name} must be [head_dim]")
-    cs = _dev(cos_sin, torch.float32, "cos_sin", 2)
-    ps = _dev(positions, torch.int64, "positions", 1)
-    if positions.shape[0] != T:
-        raise ValueError("positions length != num_tokens")
+    """What the rotation calls share: the device, the sizes, and the leading pointers."""
+    dev = _device(query, "query")
+    T, hq, d = _dims3(query, "query")
+    hkv = _dims3(key, "key")[1]
+    q, qs = _rows(dev, query, "query", T, hq, d)
+    k, ks = _rows(dev, key, "key", T, hkv, d)
+    qw = _opt(dev, q_weight, torch.bfloat16, "q_weight", d)
+    kw = _opt(dev, k_weight, torch.bfloat16, "k_weight", d)
+    cs = _arr(dev, cos_sin, torch.float32, "cos_sin", 2)
+    ps = _arr(dev, positions, torch.int64, "positions", 1, T)
     if query_out is None:
         query_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=query.device)
-    qo, qos = _rows(query_out, "query_out", hq, d, T)
-    _on_current(query, key, q_weight, k_weight, cos_sin, positions, query_out)
-    w = [None if t is None else t.data_ptr() for t in (q_weight, k_weight)]
-    return T, hq, key.shape[1], d, q, qs, k, ks, qo, qos, query_out, w, cs, ps
+    qo, qos = _rows(dev, query_out, "query_out", T, hq, d)
+    return dev, T, hq, hkv, d, query_out, qo, qos, q, qs, k, ks, (qw, kw, cs, ps)
 
 
 def qk_norm_rope(query, key, q_weight, k_weight, cos_sin, positions, *, eps: float = 1e-6, interleaved: bool = False,
                  query_out=None, key_out=None, stream=None):
     """pa_qk_norm_rope: RMS norm of every query and key head and position rotation.  Returns (query_out, key_out)."""
-    T, hq, hkv, d, q, qs, k, ks, qo, qos, query_out, w, cs, ps = _rope_args(query, key, q_weight, k_weight, cos_sin,
+    dev, T, hq, hkv, d, query_out, qo, qos, q, qs, k, ks, rest = _rope_args(query, key, q_weight, k_weight, cos_sin,
                                                                             positions, query_out)
     if key_out is None:
         key_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=key.device)
-    ko, kos = _rows(key_out, "key_out", hkv, d, T)
-    _on_current(key_out)
+    ko, kos = _rows(dev, key_out, "key_out", T, hkv, d)
     check("pa_qk_norm_rope", load().pa_qk_norm_rope(
-        qo, ko, q, k, *w, cs, ps, float(eps), qos, kos, qs, ks, cos_sin.shape[1], int(bool(interleaved)),
-        cos_sin.shape[0], T, hq, hkv, d, _stream(stream)))
+        qo, ko, q, k, *rest, float(eps), qos, kos, qs, ks, cos_sin.size(1), 1 if interleaved else 0, cos_sin.size(0),
+        T, hq, hkv, d, _raw_stream(stream, dev)))
     return query_out, key_out
 
 
 def _rope_cache(name, extra, query, key, value, q_weight, k_weight, cos_sin, positions, slot_mapping, key_cache,
                 value_cache, eps, interleaved, query_out, stream):
-    T, hq, hkv, d, q, qs, k, ks, qo, qos, query_out, w, cs, ps = _rope_args(query, key, q_weight, k_weight, cos_sin,
+    dev, T, hq, hkv, d, query_out, qo, qos, q, qs, k, ks, rest = _rope_args(query, key, q_weight, k_weight, cos_sin,
                                                                             positions, query_out)
-    v, vs = _rows(value, "value", hkv, d, T)
-    if name.endswith("int4"):
-        nb, bs, heads = _int4_dims(key_cache, value_cache, d)
+    v, vs = _rows(dev, value, "value", T, hkv, d)
+    if name == "pa_qk_norm_rope_cache_int4":
+        kc, vc, nb, bs, heads = _int4_caches(dev, key_cache, value_cache, d)
         dim = d
     else:
-        nb, bs, heads, dim = _cache_dims(key_cache, value_cache, torch.uint8 if extra else torch.bfloat16)
-    if (heads, dim) != (hkv, d):
+        dtype = torch.uint8 if extra else torch.bfloat16
+        kc, vc = _arr(dev, key_cache, dtype, "key_cache", 4), _arr(dev, value_cache, dtype, "value_cache", 4)
+        nb, bs, heads, dim = key_cache.shape
+        if value_cache.shape != key_cache.shape:
+            raise ValueError("key_cache and value_cache shapes differ")
+    if heads != hkv or dim != d:
         raise ValueError("key/value must be [num_tokens, num_kv_heads, head_dim] matching the cache")
-    sm = _dev(slot_mapping, torch.int64, "slot_mapping", 1)
-    if slot_mapping.shape[0] != T:
-        raise ValueError("slot_mapping length != num_tokens")
-    _on_current(value, slot_mapping, key_cache, value_cache)
+    sm = _arr(dev, slot_mapping, torch.int64, "slot_mapping", 1, T)
     check(name, getattr(load(), name)(
-        qo, q, k, v, *w, cs, ps, sm, key_cache.data_ptr(), value_cache.data_ptr(), float(eps), qos, qs, ks, vs,
-        cos_sin.shape[1], int(bool(interleaved)), cos_sin.shape[0], T, hq, hkv, d, bs, nb, *extra, _stream(stream)))
+        qo, q, k, v, *rest, sm, kc, vc, float(eps), qos, qs, ks, vs, cos_sin.size(1), 1 if interleaved else 0,
+        cos_sin.size(0), T, hq, hkv, d, bs, nb, *extra, _raw_stream(stream, dev)))
     return query_out
 
 
@@ -605,13 +644,6 @@ def qk_norm_rope_cache_int4(query, key, value, q_weight, k_weight, cos_sin, posi
 
 # ---- a step's tables and slots --------------------------------------------------------
 
-def _vec(t, dtype, name, n):
-    p = _dev(t, dtype, name, 1)
-    if t is not None and t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
-    return p
-
-
 def prepare_batch(block_tables, context_lens, query_lens, free_blocks, num_free, block_size: int, num_blocks: int, *,
                   seq_lens, q_start, num_free_out, status, seq_ids=None, positions=None, slot_mapping=None,
                   num_tokens: int | None = None, stream=None) -> None:
@@ -619,42 +651,37 @@ def prepare_batch(block_tables, context_lens, query_lens, free_blocks, num_free,
 
     The outputs are the caller's tensors.  The per-token arrays (seq_ids int32, positions and slot_mapping int64)
     are optional and of one length, the step's row capacity; num_tokens gives that capacity where none is passed."""
-    B = context_lens.shape[0]
-    bt = _dev(block_tables, torch.int32, "block_tables", 2)
-    if block_tables.shape[0] != B:
-        raise ValueError("block_tables rows != num_seqs")
-    per_token = [t for t in (seq_ids, positions, slot_mapping) if t is not None]
-    if num_tokens is None:
-        if not per_token:
+    dev = _device(block_tables, "block_tables")
+    i32, i64 = torch.int32, torch.int64
+    bt = _arr(dev, block_tables, i32, "block_tables", 2)
+    B, n = block_tables.size(0), num_tokens
+    if n is None:
+        first = seq_ids if seq_ids is not None else positions if positions is not None else slot_mapping
+        if first is None:
             raise ValueError("num_tokens is needed where no per-token array is passed")
-        num_tokens = per_token[0].shape[0]
-    n = int(num_tokens)
-    args = (bt, _dev(context_lens, torch.int32, "context_lens", 1), _vec(query_lens, torch.int32, "query_lens", B),
-            _dev(free_blocks, torch.int32, "free_blocks", 1), _vec(num_free, torch.int32, "num_free", 1),
-            _vec(seq_lens, torch.int32, "seq_lens", B), _vec(q_start, torch.int32, "q_start", B + 1),
-            _vec(seq_ids, torch.int32, "seq_ids", n), _vec(positions, torch.int64, "positions", n),
-            _vec(slot_mapping, torch.int64, "slot_mapping", n), _vec(num_free_out, torch.int32, "num_free_out", 1),
-            _vec(status, torch.int32, "status", 1))
-    _on_current(block_tables, context_lens, query_lens, free_blocks, num_free, seq_lens, q_start, num_free_out,
-                status, *per_token)
+        n = first.size(0)
     check("pa_prepare_batch", load().pa_prepare_batch(
-        *args, B, block_tables.shape[1], n, free_blocks.shape[0], int(block_size), int(num_blocks),
-        _stream(stream)))
+        bt, _arr(dev, context_lens, i32, "context_lens", 1, B), _arr(dev, query_lens, i32, "query_lens", 1, B),
+        _arr(dev, free_blocks, i32, "free_blocks", 1), _arr(dev, num_free, i32, "num_free", 1, 1),
+        _arr(dev, seq_lens, i32, "seq_lens", 1, B), _arr(dev, q_start, i32, "q_start", 1, B + 1),
+        _opt(dev, seq_ids, i32, "seq_ids", n), _opt(dev, positions, i64, "positions", n),
+        _opt(dev, slot_mapping, i64, "slot_mapping", n), _arr(dev, num_free_out, i32, "num_free_out", 1, 1),
+        _arr(dev, status, i32, "status", 1, 1), B, block_tables.size(1), n, free_blocks.size(0), block_size,
+        num_blocks, _raw_stream(stream, dev)))
 
 
 def release_blocks(block_tables, seq_lens, release, free_blocks, num_free, block_size: int, num_blocks: int, *,
                    status, stream=None) -> None:
     """pa_release_blocks: the blocks of the requests marked in `release` (int32) back on the free stack."""
-    B = seq_lens.shape[0]
-    bt = _dev(block_tables, torch.int32, "block_tables", 2)
-    if block_tables.shape[0] != B:
-        raise ValueError("block_tables rows != num_seqs")
-    args = (bt, _dev(seq_lens, torch.int32, "seq_lens", 1), _vec(release, torch.int32, "release", B),
-            _dev(free_blocks, torch.int32, "free_blocks", 1), _vec(num_free, torch.int32, "num_free", 1),
-            _vec(status, torch.int32, "status", 1))
-    _on_current(block_tables, seq_lens, release, free_blocks, num_free, status)
+    dev = _device(block_tables, "block_tables")
+    i32 = torch.int32
+    bt = _arr(dev, block_tables, i32, "block_tables", 2)
+    B = block_tables.size(0)
     check("pa_release_blocks", load().pa_release_blocks(
-        *args, B, block_tables.shape[1], free_blocks.shape[0], int(block_size), int(num_blocks), _stream(stream)))
+        bt, _arr(dev, seq_lens, i32, "seq_lens", 1, B), _arr(dev, release, i32, "release", 1, B),
+        _arr(dev, free_blocks, i32, "free_blocks", 1), _arr(dev, num_free, i32, "num_free", 1, 1),
+        _arr(dev, status, i32, "status", 1, 1), B, block_tables.size(1), free_blocks.size(0), block_size, num_blocks,
+        _raw_stream(stream, dev)))
 
 
 # Bytes of the fixed scratch array inside the library (PA_NOALLOC_SCRATCH_BYTES).

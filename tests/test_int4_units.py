@@ -165,6 +165,8 @@ def test_binding_refuses_wrong_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         ops.reshape_and_cache_int4(bf(3, 2, 64), bf(3, 2, 64), cache, cache, torch.zeros(3, dtype=torch.int64))
     with pytest.raises(TypeError, match="bfloat16"):
+        ops._rows(-1, torch.zeros(3, 2, 64), "query", 3, 2, 64)
+    with pytest.raises(ValueError, match="CUDA"):
         ops.qk_norm_rope(torch.zeros(3, 2, 64), bf(3, 2, 64), None, None, torch.zeros(8, 64),
                          torch.zeros(3, dtype=torch.int64))
     with pytest.raises(ValueError, match="CUDA"):
@@ -174,14 +176,17 @@ def test_binding_refuses_wrong_tensors():
 
 def test_binding_refuses_another_device(monkeypatch):
     class Fake(torch.Tensor):
-        is_cuda = True
-        device = torch.device("cuda", 1)
+        def get_device(self):
+            return 1
     t = torch.zeros(1).as_subclass(Fake)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="current device is cuda:0"):
-        ops._on_current(None, t)
+        ops._device(t, "query")
+    with pytest.raises(ValueError, match="not on cuda:0"):
+        ops._arr(0, t, torch.float32, "out", 1)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    ops._on_current(None, t)
+    assert ops._device(t, "query") == 1
+    assert ops._arr(1, t, torch.float32, "out", 1, 1) == t.data_ptr()
 
 
 def test_record_bytes():
