@@ -479,6 +479,7 @@ static int write_int4(const void *key, const void *value, int64_t key_stride, in
     p.num_kv_heads = num_kv_heads;
     p.rows = 2 * num_kv_heads;
     p.block_size = block_size;
+    p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     p.num_slots = (int64_t)num_blocks * block_size;
     return launch_rows<kCacheInt4, false>(p, head_dim, num_tokens, false, static_cast<cudaStream_t>(stream));
 }
@@ -599,6 +600,7 @@ static int qk_norm_rope_cache(void *query_out, const void *query, const void *ke
     p.value_cache = value_cache;
     p.rows += num_kv_heads;
     p.block_size = block_size;
+    p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     p.num_slots = (int64_t)num_blocks * block_size;
     p.k_inv = 1.0f / k_scale;  // rounded to fp32 once, as the FP8 cache write does
     p.v_inv = 1.0f / v_scale;

@@ -44,7 +44,7 @@ struct RowParams {
     int max_blocks;
     void *key_cache, *value_cache;
     int num_heads, num_kv_heads, rows;              // rows of one token: Hq + Hkv (+ Hkv with a cache)
-    int block_size;
+    int block_size, block_shift;                    // block_size = 1 << block_shift (4-bit cache)
     int64_t num_slots;
     float k_inv, v_inv;                             // inverse scales of an FP8 cache
     int units, chunks;                              // warps of work; per token
@@ -69,45 +69,60 @@ __device__ __forceinline__ uint4 pack8(const float *x)
                       pack_bf16x2(x[6], x[7]));
 }
 
+__device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Quantises a row spread over LPR neighbouring lanes, 8 values each: this lane's
 // 8 codes, and the row's packed (scale, zero) pair (the same in every lane).
+// Minimum and negated maximum run as one pair of bf16, a NaN prevailing.
 template <int LPR>
-__device__ __forceinline__ uint32_t quantise_row_int4(const float *x, uint32_t &pair)
+__device__ __forceinline__ uint32_t quantise_row_int4(const uint4 &raw, uint32_t &pair)
 {
-    float lo = x[0], hi = x[0];
-    bool finite = fabsf(x[0]) <= 3.402823466e38f;
+    constexpr uint32_t kSigns = 0x80008000u;
+    const uint32_t a = min_nan_bf16x2(min_nan_bf16x2(raw.x, raw.y), min_nan_bf16x2(raw.z, raw.w));
+    const uint32_t b = min_nan_bf16x2(min_nan_bf16x2(raw.x ^ kSigns, raw.y ^ kSigns),
+                                      min_nan_bf16x2(raw.z ^ kSigns, raw.w ^ kSigns));
+    uint32_t both = min_nan_bf16x2(prmt(a, b, 0x5410u), prmt(a, b, 0x7632u));
 #pragma unroll
-    for (int e = 1; e < 8; ++e) {
-        lo = fminf(lo, x[e]);
-        hi = fmaxf(hi, x[e]);
-        finite &= fabsf(x[e]) <= 3.402823466e38f;
-    }
-    if (!finite) hi = INFINITY;  // fmin and fmax would drop a NaN
-#pragma unroll
-    for (int off = LPR / 2; off >= 1; off >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-    }
+    for (int off = LPR / 2; off >= 1; off >>= 1)
+        both = min_nan_bf16x2(both, __shfl_xor_sync(0xffffffffu, both, off));
+    const float2 mm = unpack_bf16x2(both);
+    const float lo = mm.x, hi = -mm.y;
     constexpr float r15 = 1.0f / 15.0f;
     float scale = __bfloat162float(__float2bfloat16_rn(__fsub_rn(__fmul_rn(hi, r15), __fmul_rn(lo, r15))));
     float zero = lo + 0.0f;  // -0 and +0 are one minimum
-    float inv = 0.f;
-    if (!(hi < INFINITY)) {
+    if (!(hi < INFINITY && lo > -INFINITY)) {
         scale = 0.f;
         zero = __uint_as_float(0x7FC00000u);
-    } else if (scale >= 1.17549435e-38f) {
-        inv = __frcp_rn(scale);
-    } else {
-        scale = 0.f;
     }
     uint32_t codes = 0;
-    if (scale > 0.f) {
+    if (scale >= 1.17549435e-38f) {
+        const float inv = __frcp_rn(scale);
+        float x[8];
+        unpack8(raw, x);
+        // The quotient stays below 15.06 (the scale is within 2^-8 of range / 15), unless x - zero overflows.
+        // Adding 2^23 rounds to the nearest integer, ties to even: its bits are 0x4B000000 + code.
+        if (hi - lo < INFINITY) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float t = fminf(__fmul_rn(__fsub_rn(x[e], zero), inv), 15.f);
-            // adding 2^23 rounds to the nearest integer, ties to even
-            codes |= (__float_as_uint(__fadd_rn(t, 8388608.f)) & 15u) << (4 * e);
+            for (int e = 7; e >= 0; --e)
+                codes = codes * 16u + __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(x[e], zero), inv), 8388608.f));
+        } else {
+#pragma unroll 1
+            for (int w = 3; w >= 0; --w) {
+                const float2 v = unpack_bf16x2(u4_word(raw, w));
+                codes = codes * 16u +
+                        __float_as_uint(__fadd_rn(fminf(__fmul_rn(__fsub_rn(v.y, zero), inv), 15.f), 8388608.f));
+                codes = codes * 16u +
+                        __float_as_uint(__fadd_rn(fminf(__fmul_rn(__fsub_rn(v.x, zero), inv), 15.f), 8388608.f));
+            }
         }
+        codes -= 0x4B000000u * 0x11111111u;
+    } else {
+        scale = 0.f;
     }
     pair = pack_bf16x2(scale, zero);
     return codes;
@@ -142,10 +157,12 @@ __global__ void __launch_bounds__(256) row_kernel(const RowParams p)
         if (pos < 0 || pos >= p.max_position) return;  // padding: nothing is written
         const float *row = p.cos_sin + pos * p.rot;
         if constexpr (INTERLEAVED) {
-            turned = gl * 8 < p.rot;
-            if (turned) {
+            if (gl * 8 < p.rot) {
                 *reinterpret_cast<float4 *>(cs) = *reinterpret_cast<const float4 *>(row + gl * 4);
                 *reinterpret_cast<float4 *>(sn) = *reinterpret_cast<const float4 *>(row + p.rot / 2 + gl * 4);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) cs[e] = 1.f, sn[e] = 0.f;
             }
         } else {
             half = p.rot / 16;
@@ -157,6 +174,13 @@ __global__ void __launch_bounds__(256) row_kernel(const RowParams p)
                     *reinterpret_cast<float4 *>(cs + e) = *reinterpret_cast<const float4 *>(row + i + e);
                     *reinterpret_cast<float4 *>(sn + e) = *reinterpret_cast<const float4 *>(row + p.rot / 2 + i + e);
                 }
+                if (gl < half) {  // the first of a pair: a cos - b sin
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
             }
         }
     }
@@ -166,76 +190,89 @@ __global__ void __launch_bounds__(256) row_kernel(const RowParams p)
             slot = p.slots[t];
         } else {
             const int64_t pos = (int64_t)p.seq_lens[t] - 1;
-            if (pos >= 0 && pos / p.block_size < p.max_blocks) {
-                const int32_t b = p.block_tables[(int64_t)t * p.max_blocks + pos / p.block_size];
-                if (b >= 0) slot = (int64_t)b * p.block_size + pos % p.block_size;
+            if (pos >= 0 && pos >> p.block_shift < p.max_blocks) {
+                const int32_t b = p.block_tables[(int64_t)t * p.max_blocks + (pos >> p.block_shift)];
+                if (b >= 0) slot = ((int64_t)b << p.block_shift) + (pos & (p.block_size - 1));
             }
             if (c == 0 && lane == 0 && p.slots_out) p.slots_out[t] = slot;
         }
         if (slot >= p.num_slots) slot = -1;
     }
 
+    // Rows of a token: queries, keys, values.  Addresses are a token's base and the row.
+    const int r0 = c * U * GPW + grp, nq = p.num_heads, nqk = nq + p.num_kv_heads;
+    const __nv_bfloat16 *qs = p.query + (ROPE ? t * p.q_stride : 0) + gl * 8;
+    const __nv_bfloat16 *ks = p.key + t * p.k_stride + gl * 8;
+    const __nv_bfloat16 *vs = CACHE == kCacheNone ? nullptr : p.value + t * p.v_stride + gl * 8;
     uint4 raw[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int r = (c * U + i) * GPW + grp;
+        const int r = r0 + i * GPW;
         raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= p.rows) continue;
-        const __nv_bfloat16 *src;
-        if (r < p.num_heads)
-            src = p.query + t * p.q_stride + (int64_t)r * D;
-        else if (r < p.num_heads + p.num_kv_heads)
-            src = p.key + t * p.k_stride + (int64_t)(r - p.num_heads) * D;
-        else
-            src = p.value + t * p.v_stride + (int64_t)(r - p.num_heads - p.num_kv_heads) * D;
-        raw[i] = *reinterpret_cast<const uint4 *>(src + gl * 8);
+        if (r < p.rows)
+            raw[i] = *reinterpret_cast<const uint4 *>(r < nq ? qs + r * D : r < nqk ? ks + (r - nq) * D
+                                                                                    : vs + (r - nqk) * D);
+    }
+    // 4-bit cache: the row's codes and pair in head 0's records; a head is `record` bytes further on
+    const uint32_t record = CACHE == kCacheInt4 ? (uint32_t)int4_record_bytes(p.block_size, D) : 0u;
+    uint8_t *krec = nullptr, *vrec = nullptr;
+    int pair_at = 0;
+    if constexpr (CACHE == kCacheInt4) {
+        const int o = (int)(slot & (p.block_size - 1));
+        const int64_t at = (slot >> p.block_shift) * ((int64_t)p.num_kv_heads * record) + o * (D / 2) + gl * 4;
+        krec = static_cast<uint8_t *>(p.key_cache) + at;
+        vrec = static_cast<uint8_t *>(p.value_cache) + at;
+        pair_at = (p.block_size - o) * (D / 2) + o * 4;  // from the row's first byte
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int r = (c * U + i) * GPW + grp;
-        const bool is_q = r < p.num_heads;
-        const bool is_k = !is_q && r < p.num_heads + p.num_kv_heads;
-        const int h = is_q ? r : (is_k ? r - p.num_heads : r - p.num_heads - p.num_kv_heads);
+        const int r = r0 + i * GPW;
+        const bool is_q = r < nq;
+        const bool is_k = !is_q && r < nqk;
+        const int h = is_q ? r : (is_k ? r - nq : r - nqk);
         if constexpr (ROPE) {
-            float x[8], y[8];
-            unpack8(raw[i], x);
-            float ss = 0.f;
+            // values only pass through: a warp of them has nothing to do here
+            if (__any_sync(0xffffffffu, is_q || is_k)) {
+                float x[8], y[8];
+                unpack8(raw[i], x);
+                float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-            for (int off = LPR / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            const float rms = rsqrtf(ss * (1.0f / D) + p.eps);
-            const __nv_bfloat16 *w = is_q ? p.q_weight : p.k_weight;
-            float wf[8];
-            if (w) {
-                unpack8(*reinterpret_cast<const uint4 *>(w + gl * 8), wf);
-            } else {
+                for (int off = LPR / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+                const float rms = rsqrtf(ss * (1.0f / D) + p.eps);
+                const __nv_bfloat16 *w = is_q ? p.q_weight : p.k_weight;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) wf[e] = 1.f;
-            }
+                for (int e = 0; e < 8; ++e) x[e] *= rms;
+                if (w) {
+                    float wf[8];
+                    unpack8(*reinterpret_cast<const uint4 *>(w + gl * 8), wf);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * rms * wf[e];
-            if constexpr (INTERLEAVED) {
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    y[e] = turned ? x[e] * cs[e / 2] - x[e + 1] * sn[e / 2] : x[e];
-                    y[e + 1] = turned ? x[e + 1] * cs[e / 2] + x[e] * sn[e / 2] : x[e + 1];
+                    for (int e = 0; e < 8; ++e) x[e] *= wf[e];
                 }
-            } else {
-                // the pair's other element sits `half` lanes away in the row's lane group
-                const int other = grp * LPR + (gl < half ? gl + half : gl - half);
+                if constexpr (INTERLEAVED) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float o = __shfl_sync(0xffffffffu, x[e], turned ? other : lane);
-                    y[e] = turned ? (gl < half ? x[e] * cs[e] - o * sn[e] : x[e] * cs[e] + o * sn[e]) : x[e];
+                    for (int e = 0; e < 8; e += 2) {
+                        y[e] = x[e] * cs[e / 2] - x[e + 1] * sn[e / 2];
+                        y[e + 1] = x[e + 1] * cs[e / 2] + x[e] * sn[e / 2];
+                    }
+                } else {
+                    // the pair's other element sits `half` lanes away in the row's lane group
+                    const int other = !turned ? lane : grp * LPR + (gl < half ? gl + half : gl - half);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = fmaf(__shfl_sync(0xffffffffu, x[e], other), sn[e], x[e] * cs[e]);
                 }
+                // rounded to bf16 once; value rows of a mixed warp stay as they are
+                if (is_q || is_k) raw[i] = pack8(y);
             }
-            if (is_q || is_k) raw[i] = pack8(y);  // rounded to bf16 once; V rows stay as they are
         }
         const bool live = r < p.rows;
-        if (live && is_q) *reinterpret_cast<uint4 *>(p.query_out + t * p.qo_stride + (int64_t)h * D + gl * 8) = raw[i];
-        if (live && is_k && p.key_out)
-            *reinterpret_cast<uint4 *>(p.key_out + t * p.ko_stride + (int64_t)h * D + gl * 8) = raw[i];
+        if constexpr (ROPE) {
+            if (live && is_q) *reinterpret_cast<uint4 *>(p.query_out + t * p.qo_stride + h * D + gl * 8) = raw[i];
+            if constexpr (CACHE == kCacheNone)
+                if (live && is_k) *reinterpret_cast<uint4 *>(p.key_out + t * p.ko_stride + h * D + gl * 8) = raw[i];
+        }
         if constexpr (CACHE == kCacheBf16) {
             if (live && !is_q && slot >= 0)
                 *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(is_k ? p.key_cache : p.value_cache) +
@@ -256,17 +293,12 @@ __global__ void __launch_bounds__(256) row_kernel(const RowParams p)
         } else if constexpr (CACHE == kCacheInt4) {
             // a warp of query rows only has nothing to quantise
             if (__any_sync(0xffffffffu, live && !is_q)) {
-                float x[8];
-                unpack8(raw[i], x);
                 uint32_t pair;
-                const uint32_t codes = quantise_row_int4<LPR>(x, pair);
+                const uint32_t codes = quantise_row_int4<LPR>(raw[i], pair);
                 if (live && !is_q && slot >= 0) {
-                    const int64_t block = slot / p.block_size;
-                    const int o = (int)(slot - block * p.block_size);
-                    uint8_t *rec = static_cast<uint8_t *>(is_k ? p.key_cache : p.value_cache) +
-                                   (block * p.num_kv_heads + h) * int4_record_bytes(p.block_size, D);
-                    *reinterpret_cast<uint32_t *>(rec + o * (D / 2) + gl * 4) = codes;
-                    if (gl == 0) *reinterpret_cast<uint32_t *>(rec + p.block_size * (D / 2) + o * 4) = pair;
+                    uint8_t *rec = (is_k ? krec : vrec) + (uint64_t)(uint32_t)h * record;
+                    *reinterpret_cast<uint32_t *>(rec) = codes;
+                    if (gl == 0) *reinterpret_cast<uint32_t *>(rec + pair_at) = pair;
                 }
             }
         }
