@@ -429,25 +429,32 @@ static int check_int4_cache(const void *key_cache, const void *value_cache, int 
     return PA_OK;
 }
 
-template <int CACHE, bool ROPE>
+// Groups of rows from which on a warp takes 8 of them.
+static constexpr int64_t kRowsWide = 148 * 64 * 8;
+
+template <int D, int CACHE, int U>
+static int launch_rows_u(RowParams &p, int num_tokens, bool interleaved, cudaStream_t st)
+{
+    p.num_tokens = num_tokens;
+    constexpr int kRows = U * (32 / (D / 8));  // rows one warp takes
+    const int64_t chunks = cdiv64(p.rows, kRows);
+    if (chunks > 65535) return PA_ERR_BAD_SHAPE;
+    const dim3 grid((unsigned)cdiv64(num_tokens, 8), (unsigned)chunks), block(256);
+    return interleaved ? launch_pdl(row_kernel<D, CACHE, true, U>, grid, block, 0, st, p)
+                       : launch_pdl(row_kernel<D, CACHE, false, U>, grid, block, 0, st, p);
+}
+
+// Rows a warp takes, in groups of 32 / (D / 8): 8 groups spread a token's set-up
+// over more rows, 2 spread a small call over more SMs.
+template <int CACHE>
 static int launch_rows(RowParams &p, int head_dim, int num_tokens, bool interleaved, cudaStream_t st)
 {
-    const int per_warp = 4 * (32 / (head_dim / 8));  // rows one warp takes
-    p.chunks = (p.rows + per_warp - 1) / per_warp;
-    const int64_t units = (int64_t)num_tokens * p.chunks;
-    if (units > INT_MAX - 8) return PA_ERR_BAD_SHAPE;
-    p.units = (int)units;
-    const dim3 grid((unsigned)((units + 7) / 8)), block(256);
-    if constexpr (ROPE) {
-        if (interleaved)
-            return head_dim == 64 ? launch_pdl(row_kernel<64, CACHE, true, true>, grid, block, 0, st, p)
-                                  : launch_pdl(row_kernel<128, CACHE, true, true>, grid, block, 0, st, p);
-        return head_dim == 64 ? launch_pdl(row_kernel<64, CACHE, true, false>, grid, block, 0, st, p)
-                              : launch_pdl(row_kernel<128, CACHE, true, false>, grid, block, 0, st, p);
-    } else {
-        return head_dim == 64 ? launch_pdl(row_kernel<64, CACHE, false, false>, grid, block, 0, st, p)
-                              : launch_pdl(row_kernel<128, CACHE, false, false>, grid, block, 0, st, p);
-    }
+    const int64_t groups = (int64_t)num_tokens * cdiv64(p.rows, 32 / (head_dim / 8));
+    if (groups >= kRowsWide)
+        return head_dim == 64 ? launch_rows_u<64, CACHE, 8>(p, num_tokens, interleaved, st)
+                              : launch_rows_u<128, CACHE, 8>(p, num_tokens, interleaved, st);
+    return head_dim == 64 ? launch_rows_u<64, CACHE, 2>(p, num_tokens, interleaved, st)
+                          : launch_rows_u<128, CACHE, 2>(p, num_tokens, interleaved, st);
 }
 
 // K and V rows into a 4-bit cache; the slots come from `slots`, or from the
@@ -481,7 +488,16 @@ static int write_int4(const void *key, const void *value, int64_t key_stride, in
     p.block_size = block_size;
     p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     p.num_slots = (int64_t)num_blocks * block_size;
-    return launch_rows<kCacheInt4, false>(p, head_dim, num_tokens, false, static_cast<cudaStream_t>(stream));
+    const int64_t rows = (int64_t)num_tokens * p.rows, threads = rows * (head_dim / 32);
+    if (threads > INT_MAX) return PA_ERR_BAD_SHAPE;
+    p.num_rows = (uint32_t)rows;
+    // row / p.rows for row < 2^31 (p.rows >= 2): with s = ceil(log2), the multiplier floor(2^(31 + s) / rows) + 1
+    int s = 1;
+    while ((1LL << s) < p.rows) ++s;
+    p.div_mul = (uint32_t)((1ULL << (31 + s)) / (uint32_t)p.rows + 1);
+    p.div_shift = (uint32_t)(s - 1);
+    return launch_pdl(head_dim == 64 ? store_int4_kernel<64> : store_int4_kernel<128>,
+                      dim3((unsigned)cdiv64(threads, 128)), dim3(128), 0, static_cast<cudaStream_t>(stream), p);
 }
 
 // 4-bit decode workspace: arrival counters, (m, l) and the results of two cut
@@ -604,7 +620,7 @@ static int qk_norm_rope_cache(void *query_out, const void *query, const void *ke
     p.num_slots = (int64_t)num_blocks * block_size;
     p.k_inv = 1.0f / k_scale;  // rounded to fp32 once, as the FP8 cache write does
     p.v_inv = 1.0f / v_scale;
-    return launch_rows<CACHE, true>(p, head_dim, num_tokens, interleaved != 0, static_cast<cudaStream_t>(stream));
+    return launch_rows<CACHE>(p, head_dim, num_tokens, interleaved != 0, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace pakv
@@ -1200,7 +1216,7 @@ int pa_qk_norm_rope(void *query_out, void *key_out, const void *query, const voi
     if (rc != PA_OK) return rc;
     p.key_out = static_cast<__nv_bfloat16 *>(key_out);
     p.ko_stride = key_out_stride;
-    return launch_rows<kCacheNone, true>(p, head_dim, num_tokens, interleaved != 0, static_cast<cudaStream_t>(stream));
+    return launch_rows<kCacheNone>(p, head_dim, num_tokens, interleaved != 0, static_cast<cudaStream_t>(stream));
 }
 
 int pa_qk_norm_rope_cache(void *query_out, const void *query, const void *key, const void *value,
