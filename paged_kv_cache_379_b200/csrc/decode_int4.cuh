@@ -13,7 +13,6 @@
 #pragma once
 
 #include "common.cuh"
-#include "decode.cuh"
 #include "row_ops.cuh"
 
 namespace pakv {
@@ -45,24 +44,33 @@ struct Int4Lay {
     static constexpr int kSlots = D == 128 ? 2 : 4;            // stages a warp holds
     static constexpr int kRing = kSlots * kStage;
     static constexpr int kChunks = D / 16;                     // float4s a lane holds of 8 heads
+    static constexpr int kPart = NG * kChunks * 512;           // bytes of a warp's result
     static constexpr int kCtas = NG == 1 ? 4 : 3;              // resident CTAs per SM
-    static constexpr int kQf = kI4Warps * kRing;               // the unit's queries as operands
-    static constexpr int kQraw = kQf + NG * (D / 32) * 512;    // and as they are, for this unit and the next
-    static constexpr int kQrawBytes = NG * 8 * D * 2;
-    static constexpr int kBytes = kQraw + 2 * kQrawBytes;
-    static_assert(kStage >= kChunks * 32 * 16, "a warp's result for 8 heads goes through one stage");
-    static_assert(kStage >= kI4Warps * 32 * 16 + 8 * (kI4Warps * 32 / (D / 4)), "and a join of shared parts");
+    static constexpr int kQf = kI4Warps * kRing;               // each warp's queries as operands
+    static constexpr int kQfBytes = NG * (D / 32) * 512;
+    static constexpr int kHead = kQf + kI4Warps * kQfBytes;    // results of the first units of warps 1, 2, 3
+    static constexpr int kBytes = kHead + (kI4Warps - 1) * kPart;
+    static_assert(kRing >= kPart, "a warp's last result stays in its ring");
+    static_assert(kRing >= kI4Warps * 32 * 16 + 8 * (kI4Warps * 32 / (D / 4)), "and so does a join of shared parts");
     static_assert(kRec % 16 == 0 && kStage % 16 == 0, "copies are 16 bytes wide");
 };
 
 // A unit (sequence, KV head) of nt stages weighs nt + kI4UnitCost stages when the
-// work is cut into ranges: what its queries' set-up and the join of its results take.
-constexpr int kI4UnitCost = 6;
+// work is cut into ranges: what its queries' set-up and its result take.
+constexpr int kI4UnitCost = 4;
 
 // A run of stages [t0, t1) of one unit in a worker's range.
 struct Int4Seg {
     int s, h, len, nt, t0, t1, left;  // left: weight of the range behind this unit (negative: it ends in here)
-    unsigned pos;                     // stages of the range before t0 (the low bits pick the warp)
+};
+
+// A unit that a worker holds a part of, as the join needs it.
+template <int NG>
+struct Int4Cut {
+    int64_t unit;         // where it starts in the weight (its part: [NG][chunk][lane] float4, at the kept place)
+    int s, h, nt;
+    int from, to;         // it began in an earlier worker / goes on in the next; both 0: no such part
+    float qa[8 * NG], m[8 * NG], l[8 * NG];
 };
 
 __device__ __forceinline__ int int4_len(const Int4DecodeParams &p, int s, int block_size)
@@ -77,7 +85,6 @@ __device__ __forceinline__ int int4_weight(int len) { return len > 0 ? int4_stag
 // Moves to the next unit of the range; false at its end.
 __device__ __forceinline__ bool int4_next(Int4Seg &g, const Int4DecodeParams &p, int block_size)
 {
-    g.pos += g.t1 - g.t0;
     if (g.left <= kI4UnitCost) return false;
     if (++g.h == p.num_kv_heads) {
         g.h = 0;
@@ -91,6 +98,13 @@ __device__ __forceinline__ bool int4_next(Int4Seg &g, const Int4DecodeParams &p,
     g.t1 = min(g.nt, g.left - kI4UnitCost);
     g.left -= g.nt + kI4UnitCost;
     return true;
+}
+
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // 16 bytes global -> shared memory, asynchronous, past the L1.
@@ -138,12 +152,26 @@ __device__ __forceinline__ int int4_scale_exp(float vmul) { return 137 - (int)(_
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
-// The worker of position x when the weight is cut into ranges of q, the first r
-// of them one longer.
-__device__ __forceinline__ int int4_worker_of(int64_t x, int64_t q, int64_t r)
+// How the weight is cut into the workers' (warps') ranges: equal, the first `rest` of
+// them one longer.  (Shares that fall with a CTA's place on its SM, as the schedulers
+// prefer older warps, even out one launch but not launches in a row, where a CTA takes
+// the place that falls free: eight long sequences 142 instead of 134 us.)
+struct Int4Split {
+    int64_t each, rest;
+};
+
+__device__ __forceinline__ int64_t int4_begin(const Int4Split &x, int worker)
 {
-    const int64_t cut = r * (q + 1);
-    return (int)(x < cut ? x / (q + 1) : r + (x - cut) / q);
+    return worker * x.each + min((int64_t)worker, x.rest);
+}
+
+// The CTA that holds position x of `total`: a guess in floating point, then the exact one.
+__device__ __forceinline__ int int4_cta_of(const Int4Split &s, int64_t x)
+{
+    int cta = min((int)((float)x / ((float)s.each * kI4Warps)), (int)gridDim.x - 1);
+    while (int4_begin(s, cta * kI4Warps) > x) --cta;
+    while (cta + 1 < (int)gridDim.x && int4_begin(s, (cta + 1) * kI4Warps) <= x) ++cta;
+    return cta;
 }
 
 template <int D, int BS, int NG>
@@ -157,25 +185,21 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     constexpr int MT = 4 * VW;    // 16-dim tiles of the output: a lane's 2 dims each
     constexpr unsigned FULL = 0xffffffffu;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_m[W][16], s_l[W][16], s_qa[16], s_qb[16];
-    __shared__ Int4Seg s_ns[W];
-    __shared__ __align__(8) uint64_t s_bar[2];
-    __shared__ int64_t s_sum[W], s_start, s_unit, s_quot, s_rest;
-    __shared__ int s_seq, s_last;
-    __shared__ unsigned s_active;
+    __shared__ Int4Seg s_ns[W], s_seg[W];
+    __shared__ int64_t s_unit[W];
+    __shared__ Int4Split s_split;
+    __shared__ Int4Cut<NG> s_cut[W][2];   // of each warp: its first unit (if that ends in it), its last
+    __shared__ int64_t s_sum[W], s_start[W];
+    __shared__ int s_seq[W], s_first[2], s_end[2], s_last[2];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     uint8_t *const ring = smem + warp * Lay::kRing;
-    const uint32_t bars = smem_u32(s_bar), qraw32 = smem_u32(smem) + Lay::kQraw;
-    if (tid == 0) {
-        s_seq = -1;
-        mbar_init(bars, 1);
-        mbar_init(bars + 8, 1);
-        fence_mbarrier_init();
-    }
+    uint8_t *const qop = smem + Lay::kQf + warp * Lay::kQfBytes;
+    if (tid < W) s_seq[tid] = -1;
+    if (lane < 2) s_cut[warp][lane].from = s_cut[warp][lane].to = 0;
 
-    // ---- this worker's range of the weight, in (sequence, KV head, position) order
+    // ---- this worker's (warp's) range of the weight, in (sequence, KV head, position) order
     const int per = (p.num_seqs + W * 32 - 1) / (W * 32);
     const int s_lo = min(tid * per, p.num_seqs), s_hi = min(s_lo + per, p.num_seqs);
     int64_t mine = 0;
@@ -196,18 +220,26 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     }
     before *= p.num_kv_heads;
     total *= p.num_kv_heads;
-    const int workers = (int)min((int64_t)gridDim.x, max((int64_t)1, total / p.min_stages));
-    const int64_t quot = total / workers, rest = total - quot * workers;
-    const int me = blockIdx.x;
-    const int64_t lo = me * quot + min((int64_t)me, rest);
-    const int range = me < workers ? (int)(quot + (me < rest ? 1 : 0)) : 0;
-    if (range > 0 && lo >= before && lo < before + mine * p.num_kv_heads) {
+    Int4Split split;
+    int workers = gridDim.x * W;
+    if (total < (1ll << 31)) {
+        workers = max(1, min((int)total / p.min_stages, workers));
+        split.each = (int)total / workers;
+    } else {
+        workers = (int)min(total / p.min_stages, (int64_t)workers);
+        split.each = total / workers;
+    }
+    split.rest = total - split.each * workers;
+    for (int w = 0; w < W; ++w) {  // whose sequence is in here?
+        const int id = blockIdx.x * W + w;
+        const int64_t lo = int4_begin(split, id);
+        if (id >= workers || lo < before || lo >= before + mine * p.num_kv_heads) continue;
         int64_t at = before;
         for (int s = s_lo; s < s_hi; ++s) {
             const int64_t n = (int64_t)int4_weight(int4_len(p, s, BS)) * p.num_kv_heads;
             if (lo < at + n) {
-                s_seq = s;
-                s_start = at;
+                s_seq[w] = s;
+                s_start[w] = at;
                 break;
             }
             at += n;
@@ -215,29 +247,28 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     }
     __syncthreads();
 
+    const int64_t lo = int4_begin(split, blockIdx.x * W + warp);
+    const int range = (int)(int4_begin(split, blockIdx.x * W + warp + 1) - lo);
+    if (tid == 0) s_split = split;
     Int4Seg seg = {};
-    seg.s = s_seq;
+    seg.s = s_seq[warp];
     bool more = seg.s >= 0;
     if (more) {
         seg.len = int4_len(p, seg.s, BS);
         seg.nt = int4_stages(seg.len);
         const int weight = seg.nt + kI4UnitCost;
-        seg.h = (int)((lo - s_start) / weight);
-        const int64_t unit0 = s_start + (int64_t)seg.h * weight;
-        const int off = (int)(lo - unit0);
+        seg.h = (int)((lo - s_start[warp]) / weight);
+        const int64_t unit = s_start[warp] + (int64_t)seg.h * weight;
+        const int off = (int)(lo - unit);
         seg.t0 = max(0, off - kI4UnitCost);
         seg.t1 = min(seg.nt, off + range - kI4UnitCost);
         seg.left = range - (weight - off);
         more = seg.t0 < seg.t1;
-        if (tid == 0) {
-            s_unit = unit0;  // where the current unit starts in the weight
-            s_quot = quot;
-            s_rest = rest;
-        }
+        if (lane == 0) s_unit[warp] = unit;  // where the current unit starts in the weight
     }
 
     // ---- the copies.  A lane holds one table entry of the batch of stages being copied (32 entries:
-    // 32 / RECS of this warp's stages of one unit) and one of the batch after it.
+    // 32 / RECS stages of one unit) and one of the batch after it.
     constexpr int CPR = BS * D / 32;  // 16-byte chunks of a record's codes
     constexpr int PPR = BS / 4;       // and of its pairs
     const uint32_t ring32 = smem_u32(ring);
@@ -246,13 +277,18 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     int pt = 0, pend = 0, pidx = 0, ent = 0, nent = 0, nstage = -1;  // nstage: the next batch's first (-1: none)
     unsigned badmask = 0, badbatch = 0;
     auto fetch = [&](Int4Seg &ns) {  // the next batch's unit, and its entries
-        while (nstage >= ns.t1) {
+        if (nstage >= ns.t1) {
             nstage = -1;
-            if (!int4_next(ns, p, BS)) break;
-            nstage = ns.t0 + ((warp - ns.pos) & (W - 1));
+            if (int4_next(ns, p, BS)) {
+                nstage = ns.t0;
+                // its queries will be wanted soon
+                const __nv_bfloat16 *q = p.query + ((int64_t)ns.s * p.num_heads + ns.h * p.group) * D;
+                for (int i = lane * 64; i < p.group * D; i += 32 * 64)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i));
+            }
         }
         if (nstage >= 0) {  // past the end the last entry again: a stage is always copied whole
-            const int i = min((nstage + lane / RECS * W) * RECS + lane % RECS, (ns.len - 1) / BS);
+            const int i = min(nstage * RECS + lane, (ns.len - 1) / BS);
             nent = p.block_tables[(int64_t)ns.s * p.max_blocks + i];
         }
         __syncwarp();
@@ -263,7 +299,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         Int4Seg ns = s_ns[warp];
         ent = nent;
         pt = nstage;
-        pend = min(ns.t1, nstage + 32 / RECS * W);
+        pend = min(ns.t1, nstage + 32 / RECS);
         pidx = 0;
         const bool bad = (uint32_t)ent >= (uint32_t)p.num_blocks;
         badbatch = __any_sync(FULL, bad);
@@ -274,7 +310,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         const int64_t at = (int64_t)ns.h * REC + (CPR < 32 ? lane & (CPR - 1) : lane) * 16;
         pk = p.key_cache + at;
         pv = p.value_cache + at;
-        nstage += 32 / RECS * W;
+        nstage += 32 / RECS;
         fetch(ns);
     };
     // One stage into a slot, 16 bytes a lane and copy: the codes of both caches, then the pairs.
@@ -301,26 +337,16 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                     cp_async16(dv + BS * (D / 2) + chunk * 16, v + BS * (D / 2));
                 }
             }
-            pt += W;
+            ++pt;
             pidx += RECS;
             if (pt >= pend && nstage >= 0) take();
         }
         cp_async_commit();  // an empty group keeps the count where nothing is left
     };
-    // a unit's queries into buffer b
-    auto fetch_q = [&](const Int4Seg &u, int b) {
-        if (tid == 0) {
-            const uint32_t bytes = p.group * D * 2;
-            mbar_arrive_expect_tx(bars + 8 * b, bytes);
-            bulk_load(qraw32 + b * Lay::kQrawBytes, p.query + ((int64_t)u.s * p.num_heads + u.h * p.group) * D, bytes,
-                      bars + 8 * b);
-        }
-    };
     if (more) {
-        nstage = seg.t0 + ((warp - seg.pos) & (W - 1));
+        nstage = seg.t0;
         Int4Seg ns = seg;
         fetch(ns);
-        fetch_q(seg, 0);
     }
     pdl_wait();
     pdl_launch_dependents();
@@ -328,7 +354,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     for (int i = 0; i < NS; ++i) issue(i);
 
     // rows of sequences without a token
-    for (int s = me; s < p.num_seqs; s += gridDim.x)
+    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x)
         if (p.seq_lens[s] <= 0) {
             uint4 *row = reinterpret_cast<uint4 *>(p.out + (int64_t)s * p.num_heads * D);
             for (int i = tid; i < p.num_heads * D / 8; i += W * 32) row[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -354,78 +380,72 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     }
 
     int slot = 0;
-    bool dead = false;  // a wait gave up: the results become NaN
-    unsigned waited = 0;
-    for (unsigned turn = 0; more; ++turn) {
+    while (more) {
         // ---- the unit's queries: 16-bit integers, each head scaled by a power of two (its largest
         // magnitude into [2^14, 2^15)): exact for entries within 2^8 of that, the others off by at most
-        // half a step.  Warp w packs the even (w even) or odd dims of words w & ~1, w | 1 of a row's lane.
-        if (!dead && !mbar_wait_bounded(bars + 8 * (turn & 1), (turn >> 1) & 1)) {
-            dead = true;
-            waited = turn;
-            record_timeout(kTimeoutFullBarrier);
-        }
-        Int4Seg nx = seg;
-        const bool more_next = int4_next(nx, p, BS);
+        // half a step.  Bytes of the even dims of words j, j + 1 of a row's lane, then of the odd ones.
+        float qa[NG][2], qb[NG][2];
         const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             const int head = n * 8 + g;
-            const uint4 *raw = reinterpret_cast<const uint4 *>(smem + Lay::kQraw + (turn & 1) * Lay::kQrawBytes +
-                                                               (head * D + c * (D / 4)) * 2);
-            uint32_t top = 0;
-            float sum = 0.f, x[8];
+            uint4 raw[KW];
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
-                float y[8];
-                unpack8(raw[j], y);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    top = max(top, __float_as_uint(y[e]) & 0x7FFFFFFFu);
-                    sum += y[e];
-                    if ((j >> 1) == (warp >> 1) && (e & 1) == (warp & 1)) x[(j & 1) * 4 + (e >> 1)] = y[e];
-                }
+                raw[j] = make_uint4(0u, 0u, 0u, 0u);  // columns past the group are zero
+                if (head < p.group)
+                    raw[j] = *reinterpret_cast<const uint4 *>(
+                        p.query + ((int64_t)seg.s * p.num_heads + seg.h * p.group + head) * D + c * (D / 4) + 8 * j);
             }
+            uint32_t top2 = 0;
+            float sum = 0.f;
 #pragma unroll
-            for (int off = 1; off <= 2; off <<= 1) {
-                top = max(top, __shfl_xor_sync(FULL, top, off));
-                sum += __shfl_xor_sync(FULL, sum, off);
-            }
-            const int e = max((int)(top >> 23) - 127, -100);
+            for (int j = 0; j < KW; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top2 = max_nan_bf16x2(top2, u4_word(raw[j], i) & 0x7FFF7FFFu);
+            top2 = max_nan_bf16x2(top2, __shfl_xor_sync(FULL, top2, 1));
+            top2 = max_nan_bf16x2(top2, __shfl_xor_sync(FULL, top2, 2));
+            const uint32_t top = max_nan_bf16x2(top2, prmt(top2, top2, 0x1032u)) & 0x7FFFu;
+            const int e = max((int)(top >> 7) - 127, -100);
             const float mul = pow2i(max(14 - e, -126)) * sign;
-            const bool live = head < p.group;  // the other columns are zero
-            if (warp < KW) {
-                uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t v = live ? (uint32_t)__float2int_rn(x[i] * mul) : 0u;
-                    hi[i >> 2] |= ((v >> 8) & 255u) << (8 * (i & 3));
-                    lo[i >> 2] |= (v & 255u) << (8 * (i & 3));
+            for (int j = 0; j < KW; j += 2) {
+                uint32_t hi[2][2], lw[2][2];  // [odd][word]
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float x[8];
+                    unpack8(raw[j + k], x);
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        sum += x[i];
+                        v[i] = (uint32_t)__float2int_rn(x[i] * mul);
+                    }
+#pragma unroll
+                    for (int odd = 0; odd < 2; ++odd) {
+                        const uint32_t a = prmt(v[odd], v[2 + odd], 0x5140u), b = prmt(v[4 + odd], v[6 + odd], 0x5140u);
+                        lw[odd][k] = prmt(a, b, 0x5410u);
+                        hi[odd][k] = prmt(a, b, 0x7632u);
+                    }
                 }
-                *reinterpret_cast<uint4 *>(smem + Lay::kQf + ((n * KW + warp) * 32 + lane) * 16) =
-                    make_uint4(hi[0], hi[1], lo[0], lo[1]);
+#pragma unroll
+                for (int odd = 0; odd < 2; ++odd)
+                    *reinterpret_cast<uint4 *>(qop + ((n * KW + j + odd) * 32 + lane) * 16) =
+                        make_uint4(hi[odd][0], hi[odd][1], lw[odd][0], lw[odd][1]);
             }
+            sum += __shfl_xor_sync(FULL, sum, 1);
+            sum += __shfl_xor_sync(FULL, sum, 2);
             // log2-logit = qa (s S + z qb): S = +-(q . codes) 2^18 2^-e; an infinity or a NaN in the
             // query makes it NaN.  qa > 0, so the largest product is the largest logit.
-            if (warp == 0 && c == 0) {
-                s_qa[head] = live ? fminf(fmaxf(fabsf(p.scale_log2) * 3.814697265625e-6f * pow2i(min(e, 127)), 1.17549435e-38f), 3.4e38f)
-                                  : 1.f;
-                s_qb[head] = !live ? 0.f
-                                   : top >= 0x7F800000u
-                                         ? __uint_as_float(0x7FC00000u)
-                                         : sum * (sign * 262144.f) * pow2i(-(e >> 1)) * pow2i((e >> 1) - e);
-            }
-        }
-        __syncthreads();
-        if (more_next && !dead) fetch_q(nx, (turn + 1) & 1);
-        float qa[NG][2], qb[NG][2];
-#pragma unroll
-        for (int n = 0; n < NG; ++n)
+            const float a = fminf(fmaxf(fabsf(p.scale_log2) * 3.814697265625e-6f * pow2i(min(e, 127)), 1.17549435e-38f), 3.4e38f);
+            const float b = top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
+                                           : sum * (sign * 262144.f) * pow2i(-(e >> 1)) * pow2i((e >> 1) - e);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                qa[n][i] = s_qa[n * 8 + 2 * c + i];
-                qb[n][i] = s_qb[n * 8 + 2 * c + i];
+                qa[n][i] = __shfl_sync(FULL, a, (2 * c + i) * 4);
+                qb[n][i] = __shfl_sync(FULL, b, (2 * c + i) * 4);
             }
+        }
 
         float o[NG][MT][4], m[NG][2], mlim[NG][2], l[NG][2], zs[NG][2];  // m, mlim: in units of qa
 #pragma unroll
@@ -440,16 +460,18 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 l[n][i] = zs[n][i] = 0.f;
             }
         }
+        // what the stages do not need waits in shared memory
+        const int t1 = seg.t1, len = seg.len;
+        int t = seg.t0;
+        if (lane == 0) s_seg[warp] = seg;
         float vmul = 0.f;     // 2^(10 - ev): the unit's value scales are below 2^(ev + 1) so far (0: none yet)
-        bool active = false;
-        int freed = -1;       // the slot of this warp's last stage of the segment
-        bool poison = dead;
+        unsigned poison = 0;
+        __syncwarp();
 
-        for (int t = seg.t0 + ((warp - seg.pos) & (W - 1)); t < seg.t1; t += W) {
+        for (; t < t1; ++t) {
             cp_async_wait<NS - 1>();
             __syncwarp();
             poison |= (badmask >> slot) & 1u;
-            active = true;
             const uint8_t *kb = ring + slot * Lay::kStage, *vb = kb + RECS * REC;
             const uint32_t vb32 = smem_u32(vb);
 
@@ -478,8 +500,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t mask = h ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
-                            const uint4 qf = *reinterpret_cast<const uint4 *>(smem + Lay::kQf +
-                                                                              ((n * KW + j + h) * 32 + lane) * 16);
+                            const uint4 qf = *reinterpret_cast<const uint4 *>(qop + ((n * KW + j + h) * 32 + lane) * 16);
                             const uint32_t a0 = kw[0][j] & mask, a1 = kw[1][j] & mask, a2 = kw[0][j + 1] & mask,
                                            a3 = kw[1][j + 1] & mask;
                             if (j == 0) {
@@ -511,10 +532,10 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                         y = fmaf(kp.x, y, kp.y * qb[n][i]);
                     }
             }
-            if ((t + 1) * kI4Tokens > seg.len) {
+            if ((t + 1) * kI4Tokens > len) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (t * kI4Tokens + q * 8 + g >= seg.len) {
+                    if (t * kI4Tokens + q * 8 + g >= len) {
                         vp[q] = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int n = 0; n < NG; ++n) sc[q >> 1][n][(q & 1) * 2] = sc[q >> 1][n][(q & 1) * 2 + 1] = -INFINITY;
@@ -602,194 +623,275 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 }
             }
 
-            // ---- hand the slot back; the segment's last one first carries the result
+            // ---- hand the slot back
             __syncwarp();
-            if (t + W < seg.t1) {
-                issue(slot);
-            } else {
-                freed = slot;
-            }
+            issue(slot);
             if (++slot == NS) slot = 0;
         }
 
-        // ---- join the four warps: result of 8 heads at a time, [chunk][lane] float4s;
-        // chunk k of a lane: head 2c + k / (chunks / 2), dims 32 (k % (chunks / 2)) + 4 g ..
-        const bool whole = seg.t0 == 0 && seg.t1 == seg.nt;
-        const int64_t part = 2 * (int64_t)me + (seg.t0 == 0 ? 1 : 0);
-        if (tid == 0) s_active = 0;
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            if (active) {
-                if (n == 0 && lane == 0) atomicOr(&s_active, 1u << warp);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                    for (int off = 4; off <= 16; off <<= 1) {
-                        l[n][i] += __shfl_xor_sync(FULL, l[n][i], off);
-                        zs[n][i] += __shfl_xor_sync(FULL, zs[n][i], off);
-                    }
-                    if (poison) l[n][i] = __uint_as_float(0x7FC00000u);
-                    if (g == 0) {
-                        s_m[warp][n * 8 + 2 * c + i] = m[n][i];
-                        s_l[warp][n * 8 + 2 * c + i] = l[n][i];
-                    }
-                    const float f = pow2i(int4_scale_exp(vmul));  // out of the accumulators: 2^24 2^(ev - 10)
-#pragma unroll
-                    for (int k = 0; k < MT / 2; ++k) {
-                        const float4 r = make_float4(
-                            fmaf(o[n][2 * k][i] * 16384.f, f, zs[n][i]), fmaf(o[n][2 * k][2 + i] * 1024.f, f, zs[n][i]),
-                            fmaf(o[n][2 * k + 1][i] * 16384.f, f, zs[n][i]),
-                            fmaf(o[n][2 * k + 1][2 + i] * 1024.f, f, zs[n][i]));
-                        *reinterpret_cast<float4 *>(ring + freed * Lay::kStage + ((i * (MT / 2) + k) * 32 + lane) * 16) = r;
-                    }
-                }
-            }
-            // where each warp keeps its result: slots differ, so they are passed along
-            if (lane == 0) s_sum[warp] = (int64_t)(active ? warp * Lay::kRing + freed * Lay::kStage : 0);
-            __syncthreads();
-            const unsigned act = s_active;
-#pragma unroll
-            for (int k = warp; k < Lay::kChunks; k += W) {
-                const int hd = n * 8 + 2 * c + k / (Lay::kChunks / 2);
-                const int dim = 32 * (k % (Lay::kChunks / 2)) + 4 * g;
-                if (hd >= p.group) continue;
-                float M = -INFINITY, L = 0.f;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < W; ++w)
-                    if ((act >> w) & 1u) M = fmaxf(M, s_m[w][hd]);
-#pragma unroll
-                for (int w = 0; w < W; ++w)
-                    if ((act >> w) & 1u) {
-                        const float f = exp2f(s_qa[hd] * (s_m[w][hd] - M));
-                        const float4 r = *reinterpret_cast<const float4 *>(smem + s_sum[w] + (k * 32 + lane) * 16);
-                        L = fmaf(f, s_l[w][hd], L);
-                        acc.x = fmaf(f, r.x, acc.x);
-                        acc.y = fmaf(f, r.y, acc.y);
-                        acc.z = fmaf(f, r.z, acc.z);
-                        acc.w = fmaf(f, r.w, acc.w);
-                    }
-                if (whole) {
-                    const float inv = 1.f / L;
-                    *reinterpret_cast<uint2 *>(
-                        p.out + ((int64_t)seg.s * p.num_heads + seg.h * p.group + hd) * D + dim) =
-                        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                } else {
-                    p.part_o[(part * NG + n) * (Lay::kChunks * 32) + k * 32 + lane] = acc;
-                    if (g == 0 && k % (Lay::kChunks / 2) == 0) p.part_ml[part * 16 + hd] = make_float2(M, L);
-                }
-            }
-            __syncthreads();
-        }
-
-        // ---- a unit cut between workers: the last one to arrive joins its parts, in order
+        // ---- the unit's end: whole, it goes out; cut, it waits for the join
+        const Int4Seg was = s_seg[warp];
+        const int64_t here = s_unit[warp];
+        seg = was;
+        __syncwarp();
+        if (lane == 0) s_unit[warp] = here + was.nt + kI4UnitCost;
+        more = int4_next(seg, p, BS);
+        const bool whole = was.t0 == 0 && was.t1 == was.nt;
+        Int4Cut<NG> &cut = s_cut[warp][more ? 0 : 1];
+        uint8_t *data = nullptr;
+        float4 *part = nullptr;  // the first warp's first unit goes to the workspace at once
         if (!whole) {
-            const int first = seg.t0 == 0 ? me : int4_worker_of(s_unit + kI4UnitCost, s_quot, s_rest);
-            const int last = seg.t1 == seg.nt ? me : int4_worker_of(s_unit + kI4UnitCost + seg.nt - 1, s_quot, s_rest);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int n = last - first;  // arrivals before the last one
-                const int old = atomicAdd(p.counters + first, 1);
-                s_last = old == n;
-                if (old == n) p.counters[first] = 0;
+            if (!more) {
+                cp_async_wait<0>();  // nothing is left to come: the ring is free
+                __syncwarp();
+                data = ring;
+            } else if (warp > 0) {
+                data = smem + Lay::kHead + (warp - 1) * Lay::kPart;
+            } else {
+                part = p.part_o + (int64_t)2 * blockIdx.x * (NG * Lay::kChunks * 32);
             }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                // a thread per 4 dims of a head; where those are fewer than the threads, `ways` of
-                // them share the parts.  U parts are in flight at a time.
-                constexpr int U = 8;
-                const int items = p.group * (D / 4);
-                const int ways = items < W * 32 ? W * 32 / items : 1;
-                const int way = ways > 1 ? tid / items : 0;
-                uint8_t *const join = smem + s_sum[__ffs(s_active) - 1];  // a kept slot
-                for (int it = ways > 1 ? tid - way * items : tid; it < items && way < ways; it += W * 32) {
-                    const int hd = it / (D / 4), d4 = it % (D / 4);
-                    const int cell = (hd >> 3) * (Lay::kChunks * 32) +
-                                     ((hd & 1) * (D / 32) + d4 / 8) * 32 + d4 % 8 * 4 + ((hd & 7) >> 1);
-                    const float fq = s_qa[hd];
-                    float M = -INFINITY, L = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int w = first + way; w <= last; w += ways * U) {
-                        float2 ml[U];
-                        float4 r[U];
-#pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            const int x = w + u * ways;
-                            const int64_t q = 2 * x + (x == first ? 1 : 0);
-                            ml[u] = make_float2(-INFINITY, 0.f);
-                            r[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (x <= last) {
-                                ml[u] = __ldcg(&p.part_ml[q * 16 + hd]);
-                                r[u] = __ldcg(&p.part_o[q * (NG * Lay::kChunks * 32) + cell]);
-                            }
-                        }
-                        float to = M;
-#pragma unroll
-                        for (int u = 0; u < U; ++u) to = fmaxf(to, ml[u].x);
-                        const float corr = M == -INFINITY ? 0.f : exp2f(fq * (M - to));
-                        M = to;
-                        L *= corr;
-                        acc.x *= corr, acc.y *= corr, acc.z *= corr, acc.w *= corr;
-#pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            const float f = exp2f(fq * (ml[u].x - M));
-                            L = fmaf(f, ml[u].y, L);
-                            acc.x = fmaf(f, r[u].x, acc.x);
-                            acc.y = fmaf(f, r[u].y, acc.y);
-                            acc.z = fmaf(f, r[u].z, acc.z);
-                            acc.w = fmaf(f, r[u].w, acc.w);
-                        }
-                    }
-                    if (ways > 1) {
-                        *reinterpret_cast<float4 *>(join + tid * 16) = acc;
-                        if (d4 == 0) *reinterpret_cast<float2 *>(join + W * 32 * 16 + tid / (D / 4) * 8) = make_float2(M, L);
-                    } else {
-                        const float inv = 1.f / L;
-                        *reinterpret_cast<uint2 *>(
-                            p.out + ((int64_t)seg.s * p.num_heads + seg.h * p.group + hd) * D + 4 * d4) =
-                            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                    }
-                }
-                if (ways > 1) {
-                    __syncthreads();
-                    if (tid < items) {
-                        const int hd = tid / (D / 4);
-                        const float fq = s_qa[hd];
-                        const float2 *ml = reinterpret_cast<const float2 *>(join + W * 32 * 16);
-                        float M = -INFINITY, L = 0.f;
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int y = 0; y < ways; ++y) M = fmaxf(M, ml[y * p.group + hd].x);
-                        for (int y = 0; y < ways; ++y) {
-                            const float2 v = ml[y * p.group + hd];
-                            const float4 r = *reinterpret_cast<const float4 *>(join + (y * items + tid) * 16);
-                            const float f = exp2f(fq * (v.x - M));
-                            L = fmaf(f, v.y, L);
-                            acc.x = fmaf(f, r.x, acc.x);
-                            acc.y = fmaf(f, r.y, acc.y);
-                            acc.z = fmaf(f, r.z, acc.z);
-                            acc.w = fmaf(f, r.w, acc.w);
-                        }
-                        const float inv = 1.f / L;
-                        *reinterpret_cast<uint2 *>(p.out + ((int64_t)seg.s * p.num_heads + seg.h * p.group) * D + 4 * tid) =
-                            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                    }
-                    __syncthreads();
-                }
+            if (lane == 0) {
+                cut.unit = here;
+                cut.s = was.s;
+                cut.h = was.h;
+                cut.nt = was.nt;
+                cut.from = was.t0 > 0;
+                cut.to = was.t1 < was.nt;
             }
         }
-
-        // ---- the kept slot can be filled again
-        if (freed >= 0) issue(freed);
-        if (tid == 0) s_unit += seg.nt + kI4UnitCost;  // read behind the next join's barriers
-        seg = nx;
-        more = more_next;
+        const float f = pow2i(int4_scale_exp(vmul));  // out of the accumulators: 2^24 2^(ev - 10)
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int hd = n * 8 + 2 * c + i;
+#pragma unroll
+                for (int off = 4; off <= 16; off <<= 1) {
+                    l[n][i] += __shfl_xor_sync(FULL, l[n][i], off);
+                    zs[n][i] += __shfl_xor_sync(FULL, zs[n][i], off);
+                }
+                if (poison) l[n][i] = __uint_as_float(0x7FC00000u);
+                const float inv = 1.f / l[n][i];
+                if (!whole && g == 0) {
+                    cut.qa[hd] = qa[n][i];
+                    cut.m[hd] = m[n][i];
+                    cut.l[hd] = l[n][i];
+                    if (part && hd < p.group) p.part_ml[2 * blockIdx.x * 16 + hd] = make_float2(m[n][i], l[n][i]);
+                }
+#pragma unroll
+                for (int k = 0; k < MT / 2; ++k) {  // dims 32 k + 4 g ..
+                    const float4 r = make_float4(
+                        fmaf(o[n][2 * k][i] * 16384.f, f, zs[n][i]), fmaf(o[n][2 * k][2 + i] * 1024.f, f, zs[n][i]),
+                        fmaf(o[n][2 * k + 1][i] * 16384.f, f, zs[n][i]),
+                        fmaf(o[n][2 * k + 1][2 + i] * 1024.f, f, zs[n][i]));
+                    const int cell = (n * Lay::kChunks + i * (MT / 2) + k) * 32 + lane;
+                    if (hd >= p.group) continue;
+                    if (whole)
+                        *reinterpret_cast<uint2 *>(
+                            p.out + ((int64_t)was.s * p.num_heads + was.h * p.group + hd) * D + 32 * k + 4 * g) =
+                            make_uint2(pack_bf16x2(r.x * inv, r.y * inv), pack_bf16x2(r.z * inv, r.w * inv));
+                    else if (part)
+                        part[cell] = r;
+                    else
+                        *reinterpret_cast<float4 *>(data + cell * 16) = r;
+                }
+            }
     }
     cp_async_wait<0>();
-    // a wait for the queries that gave up: the copy may still be on its way (one more bounded wait)
-    if (dead && !mbar_wait_bounded(bars + 8 * (waited & 1), (waited >> 1) & 1)) record_timeout(kTimeoutDrain);
+    __syncthreads();
+
+    // ---- the join.  Parts of one unit lie in neighbouring warps: a run of them is joined here, and
+    // what is still only a part of its unit goes to the workspace (slot 0: began before this CTA,
+    // 1: begins in it).  Part 2 w + k is warp w's first (0) or last (1) unit.
+    unsigned have = 0, from = 0, to = 0;
+#pragma unroll
+    for (int e = 0; e < 2 * W; ++e) {
+        const Int4Cut<NG> &u = s_cut[e >> 1][e & 1];
+        if (u.from) from |= 1u << e;
+        if (u.to) to |= 1u << e;
+    }
+    have = from | to;
+    if (!have) return;
+    // the run that part e lies in: up to the first part (from e on) that does not go on, down to the
+    // last one (up to e) that did not come from before.  Part 0 stands alone, in the workspace already.
+    auto run_of = [&](int e) {
+        unsigned r = 1u << e;
+        for (int x = e; (to >> x) & 1u;) {
+            const unsigned next = have & (~1u << x);
+            if (!next) break;
+            x = __ffs(next) - 1;
+            r |= 1u << x;
+        }
+        for (int x = e; (from >> x) & 1u;) {
+            const unsigned prev = have & ((1u << x) - 1) & ~1u;
+            if (!prev) break;
+            x = 31 - __clz(prev);
+            r |= 1u << x;
+        }
+        return r;
+    };
+    float *const wf = reinterpret_cast<float *>(smem + Lay::kQf);  // [part][head]: the queries are done with
+    constexpr int H = 8 * NG;
+    if (tid < 2 * W * H && (have >> (tid / H)) & 1u) {
+        const int e = tid / H, hd = tid % H;
+        const unsigned r = run_of(e);
+        float M = -INFINITY;
+        for (unsigned b = r; b; b &= b - 1) M = fmaxf(M, s_cut[(__ffs(b) - 1) >> 1][(__ffs(b) - 1) & 1].m[hd]);
+        const float fq = s_cut[e >> 1][e & 1].qa[hd];
+        wf[tid] = fast_exp2(fq * (s_cut[e >> 1][e & 1].m[hd] - M));
+        float L = 0.f;
+        for (unsigned b = r; b; b &= b - 1) {
+            const Int4Cut<NG> &u = s_cut[(__ffs(b) - 1) >> 1][(__ffs(b) - 1) & 1];
+            L = fmaf(fast_exp2(fq * (u.m[hd] - M)), u.l[hd], L);
+        }
+        wf[2 * W * H + tid] = L;
+        wf[4 * W * H + tid] = M;
+    }
+    __syncthreads();
+    int left = have & 1u ? 0 : -1, right = -1;  // a part of the unit shared with earlier / later CTAs
+    for (unsigned todo = have & ~1u; todo;) {
+        const int e0 = __ffs(todo) - 1;
+        const unsigned r = run_of(e0);
+        todo &= ~r;
+        const int e1 = 31 - __clz(r);
+        const bool before_me = (from >> e0) & 1u, behind = (to >> e1) & 1u;
+        if (before_me) left = e0;
+        if (behind) right = e0;
+        const Int4Cut<NG> &u = s_cut[e0 >> 1][e0 & 1];
+        const int64_t part = 2 * blockIdx.x + (before_me ? 0 : 1);
+        for (int cell = tid; cell < NG * Lay::kChunks * 32; cell += W * 32) {
+            const int k = (cell >> 5) % Lay::kChunks, hd = (cell >> 5) / Lay::kChunks * 8 + 2 * c + k / (MT / 2);
+            if (hd >= p.group) continue;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (unsigned b = r; b; b &= b - 1) {
+                const int e = __ffs(b) - 1;
+                const uint8_t *d = e & 1 ? smem + (e >> 1) * Lay::kRing : smem + Lay::kHead + ((e >> 1) - 1) * Lay::kPart;
+                const float4 v = *reinterpret_cast<const float4 *>(d + cell * 16);
+                const float f = wf[e * H + hd];
+                acc.x = fmaf(f, v.x, acc.x);
+                acc.y = fmaf(f, v.y, acc.y);
+                acc.z = fmaf(f, v.z, acc.z);
+                acc.w = fmaf(f, v.w, acc.w);
+            }
+            const float L = wf[2 * W * H + e0 * H + hd];
+            if (!before_me && !behind) {
+                const float inv = 1.f / L;
+                *reinterpret_cast<uint2 *>(p.out + ((int64_t)u.s * p.num_heads + u.h * p.group + hd) * D +
+                                           32 * (k % (MT / 2)) + 4 * g) =
+                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            } else {
+                p.part_o[part * (NG * Lay::kChunks * 32) + cell] = acc;
+                if (g == 0 && k % (MT / 2) == 0) p.part_ml[part * 16 + hd] = make_float2(wf[4 * W * H + e0 * H + hd], L);
+            }
+        }
+    }
+    if (left < 0 && right < 0) return;
+
+    // ---- a unit cut between CTAs: the last one to arrive joins its parts, in order
+    if (left == right) right = -1;
+    __syncthreads();
+    if (lane == 0 && warp < 2) {
+        const int e = warp ? right : left;
+        if (e >= 0) {
+            const Int4Cut<NG> &u = s_cut[e >> 1][e & 1];
+            const int first = from >> e & 1u ? int4_cta_of(s_split, u.unit + kI4UnitCost) : blockIdx.x;
+            const int last = int4_cta_of(s_split, u.unit + kI4UnitCost + u.nt - 1);
+            const int n = last - first;  // arrivals before the last one
+            __threadfence();  // the CTA's part, behind the barrier above
+            const int old = atomicAdd(p.counters + first, 1);
+            __threadfence();  // the others' parts, ahead of the barrier below
+            s_last[warp] = old == n;
+            if (old == n) p.counters[first] = 0;
+            s_first[warp] = first;
+            s_end[warp] = last;
+        }
+    }
+    __syncthreads();
+    for (int side = 0; side < 2; ++side) {
+        const int e = side ? right : left;
+        if (e < 0 || !s_last[side]) continue;
+        const Int4Cut<NG> *u = &s_cut[e >> 1][e & 1];
+        const int first = s_first[side], last = s_end[side];
+        const int items = p.group * (D / 4);
+        // a thread per 4 dims of a head; where those are fewer than the threads, `ways` of
+        // them share the parts.  U parts are in flight at a time.
+        constexpr int U = 8;
+        const int ways = items < W * 32 ? W * 32 / items : 1;
+        const int way = ways > 1 ? tid / items : 0;
+        uint8_t *const join = smem + side * Lay::kRing;  // rings are free
+        for (int it = ways > 1 ? tid - way * items : tid; it < items && way < ways; it += W * 32) {
+            const int hd = it / (D / 4), d4 = it % (D / 4);
+            const int cell = ((hd >> 3) * Lay::kChunks + (hd & 1) * (D / 32) + d4 / 8) * 32 + d4 % 8 * 4 + ((hd & 7) >> 1);
+            const float fq = u->qa[hd];
+            float M = -INFINITY, L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = first + way; w <= last; w += ways * U) {
+                float2 ml[U];
+                float4 r[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int x = w + u * ways;
+                    const int64_t q = 2 * x + (x == first ? 1 : 0);
+                    ml[u] = make_float2(-INFINITY, 0.f);
+                    r[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (x <= last) {
+                        ml[u] = __ldcg(&p.part_ml[q * 16 + hd]);
+                        r[u] = __ldcg(&p.part_o[q * (NG * Lay::kChunks * 32) + cell]);
+                    }
+                }
+                float to = M;
+#pragma unroll
+                for (int u = 0; u < U; ++u) to = fmaxf(to, ml[u].x);
+                const float corr = M == -INFINITY ? 0.f : exp2f(fq * (M - to));
+                M = to;
+                L *= corr;
+                acc.x *= corr, acc.y *= corr, acc.z *= corr, acc.w *= corr;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float f = fast_exp2(fq * (ml[u].x - M));
+                    L = fmaf(f, ml[u].y, L);
+                    acc.x = fmaf(f, r[u].x, acc.x);
+                    acc.y = fmaf(f, r[u].y, acc.y);
+                    acc.z = fmaf(f, r[u].z, acc.z);
+                    acc.w = fmaf(f, r[u].w, acc.w);
+                }
+            }
+            if (ways > 1) {
+                *reinterpret_cast<float4 *>(join + tid * 16) = acc;
+                if (d4 == 0) *reinterpret_cast<float2 *>(join + W * 32 * 16 + tid / (D / 4) * 8) = make_float2(M, L);
+            } else {
+                const float inv = 1.f / L;
+                *reinterpret_cast<uint2 *>(
+                    p.out + ((int64_t)u->s * p.num_heads + u->h * p.group + hd) * D + 4 * d4) =
+                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            }
+        }
+        if (ways > 1) {
+            __syncthreads();
+            if (tid < items) {
+                const int hd = tid / (D / 4);
+                const float fq = u->qa[hd];
+                const float2 *ml = reinterpret_cast<const float2 *>(join + W * 32 * 16);
+                float M = -INFINITY, L = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int y = 0; y < ways; ++y) M = fmaxf(M, ml[y * p.group + hd].x);
+                for (int y = 0; y < ways; ++y) {
+                    const float2 v = ml[y * p.group + hd];
+                    const float4 r = *reinterpret_cast<const float4 *>(join + (y * items + tid) * 16);
+                    const float f = fast_exp2(fq * (v.x - M));
+                    L = fmaf(f, v.y, L);
+                    acc.x = fmaf(f, r.x, acc.x);
+                    acc.y = fmaf(f, r.y, acc.y);
+                    acc.z = fmaf(f, r.z, acc.z);
+                    acc.w = fmaf(f, r.w, acc.w);
+                }
+                const float inv = 1.f / L;
+                *reinterpret_cast<uint2 *>(p.out + ((int64_t)u->s * p.num_heads + u->h * p.group) * D + 4 * tid) =
+                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            }
+            __syncthreads();
+        }
+    }
 }
 
 }  // namespace pakv

@@ -517,11 +517,11 @@ static Int4Workspace int4_workspace(int group, int head_dim)
     return w;
 }
 
-// Fewest stages (32 tokens of one KV head) worth a worker of its own.
+// Fewest stages (32 tokens of one KV head) worth a warp of their own.
 static constexpr int kI4MinStages = 4;
 
 template <int D, int BS, int NG>
-static int launch_decode_int4_t(const Int4DecodeParams &p, int workers, cudaStream_t st)
+static int launch_decode_int4_t(Int4DecodeParams &p, int workers, cudaStream_t st)
 {
     using Lay = Int4Lay<D, BS, NG>;
     auto kernel = decode_int4_kernel<D, BS, NG>;
@@ -529,13 +529,14 @@ static int launch_decode_int4_t(const Int4DecodeParams &p, int workers, cudaStre
     if (rc != PA_OK) return rc;
     const int sms = sm_count();
     if (sms < 1) return check_cuda(cudaErrorInvalidConfiguration);
-    const int64_t most = (int64_t)p.num_seqs * p.num_kv_heads * cdiv64((int64_t)p.max_blocks * BS, kI4Tokens);
-    const int64_t grid = std::min<int64_t>({workers, (int64_t)sms * Lay::kCtas, cdiv64(most, p.min_stages)});
+    const int64_t most = (int64_t)p.num_seqs * p.num_kv_heads *
+                         (cdiv64((int64_t)p.max_blocks * BS, kI4Tokens) + kI4UnitCost);
+    const int64_t grid = std::min<int64_t>({workers, (int64_t)sms * Lay::kCtas, cdiv64(most, p.min_stages * kI4Warps)});
     return launch_pdl(kernel, dim3((unsigned)grid), dim3(kI4Warps * 32), Lay::kBytes, st, p);
 }
 
 template <int D>
-static int launch_decode_int4_d(int block_size, const Int4DecodeParams &p, int workers, cudaStream_t st)
+static int launch_decode_int4_d(int block_size, Int4DecodeParams &p, int workers, cudaStream_t st)
 {
     switch (block_size * 2 + (p.group > 8)) {
     case 16: return launch_decode_int4_t<D, 8, 1>(p, workers, st);
