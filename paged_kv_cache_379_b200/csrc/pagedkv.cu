@@ -417,6 +417,16 @@ static int check_rows(const void *ptr, int64_t stride, int heads, int d, int num
     return PA_OK;
 }
 
+// n / d = umulhi(n, mul) >> shift for 0 <= n < 2^31: mul = floor(2^(31 + s) / d) + 1 and
+// shift = s - 1 with s = ceil(log2 d); mul 0 for d = 1.
+static void divisor(int d, uint32_t &mul, uint32_t &shift)
+{
+    int s = 1;
+    while ((1LL << s) < d) ++s;
+    mul = d == 1 ? 0u : (uint32_t)((1ULL << (31 + s)) / (uint32_t)d + 1);
+    shift = (uint32_t)(s - 1);
+}
+
 static int check_int4_cache(const void *key_cache, const void *value_cache, int num_kv_heads, int head_dim,
                             int block_size, int num_blocks)
 {
@@ -491,11 +501,7 @@ static int write_int4(const void *key, const void *value, int64_t key_stride, in
     const int64_t rows = (int64_t)num_tokens * p.rows, threads = rows * (head_dim / 32);
     if (threads > INT_MAX) return PA_ERR_BAD_SHAPE;
     p.num_rows = (uint32_t)rows;
-    // row / p.rows for row < 2^31 (p.rows >= 2): with s = ceil(log2), the multiplier floor(2^(31 + s) / rows) + 1
-    int s = 1;
-    while ((1LL << s) < p.rows) ++s;
-    p.div_mul = (uint32_t)((1ULL << (31 + s)) / (uint32_t)p.rows + 1);
-    p.div_shift = (uint32_t)(s - 1);
+    divisor(p.rows, p.div_mul, p.div_shift);
     return launch_pdl(head_dim == 64 ? store_int4_kernel<64> : store_int4_kernel<128>,
                       dim3((unsigned)cdiv64(threads, 128)), dim3(128), 0, static_cast<cudaStream_t>(stream), p);
 }
@@ -1347,8 +1353,14 @@ int pa_prepare_batch(int32_t *block_tables, const int32_t *context_lens, const i
     p.num_blocks = num_blocks;
     p.free_capacity = free_capacity;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool fused = num_tokens <= kBatchFusedTokens;
-    const int rc = launch_pdl(prepare_batch_kernel, dim3(1), dim3(kBatchThreads), 0, st, p, fused ? 1 : 0);
+    divisor(block_size, p.div_mul, p.div_shift);
+    // several CTAs where no output is an input, and a request's sums fit each one's copy
+    auto apart = [](const int32_t *a, const int32_t *b, int n) { return a + n <= b || b + n <= a; };
+    const bool alone = !apart(seq_lens, context_lens, num_seqs) || !apart(seq_lens, query_lens, num_seqs) ||
+                       num_free_out == num_free || num_seqs > kBatchSmemSeqs;
+    const bool fused = !alone || num_tokens <= kBatchFusedTokens;
+    const unsigned ctas = alone ? 1u : std::max(1u, (unsigned)cdiv64(num_tokens, kBatchRows));
+    const int rc = launch_pdl(prepare_batch_kernel, dim3(ctas), dim3(kBatchThreads), 0, st, p, fused ? 1 : 0);
     if (rc != PA_OK || fused) return rc;
     return launch_pdl(fill_tokens_kernel, dim3((unsigned)cdiv64(num_tokens, 1024)), dim3(256), 0, st, p);
 }

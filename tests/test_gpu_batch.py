@@ -270,3 +270,25 @@ def test_chunk_over_4bit_context_by_prefill():
     mag = float(q[-1].double().abs().sum(-1).max() * k * 0.088) * 2.0 ** -8
     v = float(vb.cpu().double().abs().amax())
     assert float((out[-1].double() - tok[0].double()).abs().max()) <= 2 * mag * v + 3 * v * 2.0 ** -8
+
+
+@pytest.mark.parametrize("B,new_high", [(7, 3), (64, 400), (1500, 9)])
+def test_prepare_in_place_equals_apart(B, new_high):
+    """Lengths and the free count updated in place: the same integers, small steps and large ones."""
+    a, b = (_batch(B, 100, 0, new_high, 16, B) for _ in range(2))
+    want = a.run()
+    got = b.run(seq_lens=b.d["context_lens"], num_free_out=b.d["num_free"])
+    assert torch.equal(a.d["block_tables"], b.d["block_tables"])
+    for k in want:
+        assert (want[k] == got[k]).all(), k
+    a.check(want)
+
+
+def test_prepare_largest_rows():
+    """The last positions of the widest row (15 blocks of 2^27: a 16th would pass 31 bits), one token past it,
+    and a block size of one."""
+    s = Step([15 * 2 ** 27 - 40], [9], 1 << 27, 40, 15, 12)
+    s.check(s.run())
+    _refused(Step([15 * 2 ** 27 - 8], [9], 1 << 27, 40, 15, 12), -2)
+    s = Step([5, 0, 3], [2, 0, 4], 1, 40, 9, 8)
+    s.check(s.run())
