@@ -703,86 +703,72 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     // ---- the join.  Parts of one unit lie in neighbouring warps: a run of them is joined here, and
     // what is still only a part of its unit goes to the workspace (slot 0: began before this CTA,
     // 1: begins in it).  Part 2 w + k is warp w's first (0) or last (1) unit.
-    unsigned have = 0, from = 0, to = 0;
-#pragma unroll
-    for (int e = 0; e < 2 * W; ++e) {
-        const Int4Cut<NG> &u = s_cut[e >> 1][e & 1];
-        if (u.from) from |= 1u << e;
-        if (u.to) to |= 1u << e;
-    }
-    have = from | to;
+    const Int4Cut<NG> &mine_cut = s_cut[(lane >> 1) % W][lane & 1];
+    const unsigned from = __ballot_sync(FULL, lane < 2 * W && mine_cut.from);
+    const unsigned to = __ballot_sync(FULL, lane < 2 * W && mine_cut.to);
+    const unsigned have = from | to;
     if (!have) return;
-    // the run that part e lies in: up to the first part (from e on) that does not go on, down to the
-    // last one (up to e) that did not come from before.  Part 0 stands alone, in the workspace already.
-    auto run_of = [&](int e) {
-        unsigned r = 1u << e;
-        for (int x = e; (to >> x) & 1u;) {
-            const unsigned next = have & (~1u << x);
-            if (!next) break;
-            x = __ffs(next) - 1;
-            r |= 1u << x;
-        }
-        for (int x = e; (from >> x) & 1u;) {
-            const unsigned prev = have & ((1u << x) - 1) & ~1u;
-            if (!prev) break;
-            x = 31 - __clz(prev);
-            r |= 1u << x;
-        }
-        return r;
-    };
+    // Part 0 is in the workspace already.  The others' runs begin where no earlier part belongs to the unit.
+    const unsigned parts = have & ~1u, begins = parts & (~from | (parts & -parts));
     float *const wf = reinterpret_cast<float *>(smem + Lay::kQf);  // [part][head]: the queries are done with
     constexpr int H = 8 * NG;
-    if (tid < 2 * W * H && (have >> (tid / H)) & 1u) {
+    auto run_of = [&](int e) {  // the parts of e's run
+        const int b = 31 - __clz(begins & (2u << e) - 1);
+        const unsigned after = begins & ~((2u << e) - 1);
+        return parts & ~((1u << b) - 1) & (after ? (after & -after) - 1 : ~0u);
+    };
+    if (tid < 2 * W * H && (parts >> tid / H & 1u)) {
         const int e = tid / H, hd = tid % H;
-        const unsigned r = run_of(e);
-        float M = -INFINITY;
-        for (unsigned b = r; b; b &= b - 1) M = fmaxf(M, s_cut[(__ffs(b) - 1) >> 1][(__ffs(b) - 1) & 1].m[hd]);
         const float fq = s_cut[e >> 1][e & 1].qa[hd];
-        wf[tid] = fast_exp2(fq * (s_cut[e >> 1][e & 1].m[hd] - M));
-        float L = 0.f;
-        for (unsigned b = r; b; b &= b - 1) {
-            const Int4Cut<NG> &u = s_cut[(__ffs(b) - 1) >> 1][(__ffs(b) - 1) & 1];
-            L = fmaf(fast_exp2(fq * (u.m[hd] - M)), u.l[hd], L);
+        const unsigned run = run_of(e);
+        float M = -INFINITY, L = 0.f;
+        for (unsigned b = run; b; b &= b - 1) M = fmaxf(M, s_cut[__ffs(b) - 1 >> 1][__ffs(b) - 1 & 1].m[hd]);
+        for (unsigned b = run; b; b &= b - 1) {
+            const Int4Cut<NG> &u = s_cut[__ffs(b) - 1 >> 1][__ffs(b) - 1 & 1];
+            const float f = fast_exp2(fq * (u.m[hd] - M));
+            L = fmaf(f, u.l[hd], L);
+            if (__ffs(b) - 1 == e) wf[tid] = f;
         }
         wf[2 * W * H + tid] = L;
         wf[4 * W * H + tid] = M;
     }
     __syncthreads();
-    int left = have & 1u ? 0 : -1, right = -1;  // a part of the unit shared with earlier / later CTAs
-    for (unsigned todo = have & ~1u; todo;) {
-        const int e0 = __ffs(todo) - 1;
-        const unsigned r = run_of(e0);
-        todo &= ~r;
-        const int e1 = 31 - __clz(r);
-        const bool before_me = (from >> e0) & 1u, behind = (to >> e1) & 1u;
-        if (before_me) left = e0;
-        if (behind) right = e0;
-        const Int4Cut<NG> &u = s_cut[e0 >> 1][e0 & 1];
-        const int64_t part = 2 * blockIdx.x + (before_me ? 0 : 1);
-        for (int cell = tid; cell < NG * Lay::kChunks * 32; cell += W * 32) {
-            const int k = (cell >> 5) % Lay::kChunks, hd = (cell >> 5) / Lay::kChunks * 8 + 2 * c + k / (MT / 2);
-            if (hd >= p.group) continue;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (unsigned b = r; b; b &= b - 1) {
-                const int e = __ffs(b) - 1;
-                const uint8_t *d = e & 1 ? smem + (e >> 1) * Lay::kRing : smem + Lay::kHead + ((e >> 1) - 1) * Lay::kPart;
-                const float4 v = *reinterpret_cast<const float4 *>(d + cell * 16);
-                const float f = wf[e * H + hd];
-                acc.x = fmaf(f, v.x, acc.x);
-                acc.y = fmaf(f, v.y, acc.y);
-                acc.z = fmaf(f, v.z, acc.z);
-                acc.w = fmaf(f, v.w, acc.w);
-            }
-            const float L = wf[2 * W * H + e0 * H + hd];
-            if (!before_me && !behind) {
+    // A part of the unit shared with earlier / later CTAs, or -1: the first run's, the last one's.
+    const int first_part = __ffs(parts) - 1, last_part = 31 - __clz(parts);  // -1: none
+    const int left = have & 1u ? 0 : first_part >= 0 && (from >> first_part & 1u) ? first_part : -1;
+    int right = last_part >= 0 && (to >> last_part & 1u) ? 31 - __clz(begins) : -1;
+    for (int cell = tid; cell < NG * Lay::kChunks * 32; cell += W * 32) {
+        const int k = (cell >> 5) % Lay::kChunks, hd = (cell >> 5) / Lay::kChunks * 8 + 2 * c + k / (MT / 2);
+        if (hd >= p.group) continue;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (unsigned b = parts; b;) {
+            const int e = __ffs(b) - 1;
+            b &= b - 1;
+            const float4 v = *reinterpret_cast<const float4 *>(
+                smem + (e & 1 ? (e >> 1) * Lay::kRing : Lay::kHead + ((e >> 1) - 1) * Lay::kPart) + cell * 16);
+            const float f = wf[e * H + hd];
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
+            const bool ends = !b || (begins >> (__ffs(b) - 1) & 1u);
+            if (!ends) continue;
+            // the run's last part: out it goes
+            const float L = wf[2 * W * H + e * H + hd];
+            const int b0 = 31 - __clz(begins & (2u << e) - 1);
+            if (b0 != left && b0 != right) {
+                const Int4Cut<NG> &u = s_cut[e >> 1][e & 1];
                 const float inv = 1.f / L;
                 *reinterpret_cast<uint2 *>(p.out + ((int64_t)u.s * p.num_heads + u.h * p.group + hd) * D +
                                            32 * (k % (MT / 2)) + 4 * g) =
                     make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
             } else {
+                const int64_t part = 2 * blockIdx.x + (b0 == left ? 0 : 1);
                 p.part_o[part * (NG * Lay::kChunks * 32) + cell] = acc;
-                if (g == 0 && k % (MT / 2) == 0) p.part_ml[part * 16 + hd] = make_float2(wf[4 * W * H + e0 * H + hd], L);
+                if (g == 0 && k % (MT / 2) == 0) p.part_ml[part * 16 + hd] = make_float2(wf[4 * W * H + e * H + hd], L);
             }
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
     if (left < 0 && right < 0) return;
@@ -815,7 +801,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         const int items = p.group * (D / 4);
         // a thread per 4 dims of a head; where those are fewer than the threads, `ways` of
         // them share the parts.  U parts are in flight at a time.
-        constexpr int U = 8;
+        constexpr int U = 4;
         const int ways = items < W * 32 ? W * 32 / items : 1;
         const int way = ways > 1 ? tid / items : 0;
         uint8_t *const join = smem + side * Lay::kRing;  // rings are free
