@@ -9,6 +9,24 @@
 // is an integer of 16 bits in two bytes.  Value product: a nibble in bits 0-3 of a
 // half word is the fp16 subnormal c 2^-24, one in bits 4-7 is 16 c 2^-24, so one AND
 // gives two exact operands, and the 16 comes out of the accumulator.
+//
+// Work: a unit is one sequence and KV head, a stage 32 of its tokens.  The weight of
+// all units is cut into equal ranges, one for each warp of the grid, so a long
+// sequence spreads over the GPU and short ones share a warp; a warp runs through its
+// range alone, with its own ring of stages (cp.async, 16 bytes a lane: the records'
+// bulk copies took 581 instead of 565 instructions a stage) and its own online
+// softmax.  Units cut between warps are joined once, at the CTA's end, and between
+// CTAs by the last of them to arrive, in a fixed order.  (Ranges for CTAs, whose
+// warps take turns at a unit's stages and join at its end: 48.9 instead of 43.7 us
+// for the grouped-query batch, 8.7 instead of 3.8 for four short sequences.)
+//
+// Bound, head_dim 128 and block_size 16, one launch after another: eight sequences of
+// 32K-128K tokens (713 MB) 131 us, 83 % of the measured copy rate, its stages at that
+// rate and the rest the start (4 us) and the join; 128 sequences of ~1100 tokens, 8
+// query heads on each of 8 KV heads (160 MB) 42 us, 64 sequences with 32 heads (323
+// MB) 69 us: 26 and 51 us of stages, 4 of start, the rest the join, where the SMs
+// wait for their last warps and for cold code.  A stage takes about 440
+// instructions; the pipe of the ANDs is the fullest (57 %).
 // Included once, by pagedkv.cu.
 #pragma once
 
@@ -19,8 +37,8 @@ namespace pakv {
 
 constexpr int kI4Warps = 4;
 constexpr int kI4Tokens = 32;        // tokens of one stage
-constexpr int kI4MaxWorkers = 592;   // CTAs with partial results: 148 SMs x 4
-constexpr int kI4HeaderBytes = 4096; // workspace: arrival counters of the workers
+constexpr int kI4MaxCtas = 592;      // CTAs with partial results: 148 SMs x 4
+constexpr int kI4HeaderBytes = 4096; // workspace: arrival counters of the CTAs
 
 struct Int4DecodeParams {
     __nv_bfloat16 *out;                 // [B, Hq, D]
@@ -28,9 +46,9 @@ struct Int4DecodeParams {
     const uint8_t *key_cache, *value_cache;
     const int32_t *block_tables;        // [B, max_blocks]
     const int32_t *seq_lens;            // [B]
-    int *counters;                      // [workers], zero between calls
-    float2 *part_ml;                    // [2 workers][16] (m, l)
-    float4 *part_o;                     // [2 workers][NG * D/16 chunks][32 lanes]
+    int *counters;                      // [CTAs], zero between calls
+    float2 *part_ml;                    // [2 CTAs][16] (m, l)
+    float4 *part_o;                     // [2 CTAs][NG * D/16 chunks][32 lanes]
     float scale_log2;                   // scale * log2(e)
     int num_seqs, num_heads, num_kv_heads, group, max_blocks, num_blocks, min_stages;
     int c16, c256;                      // 16 and 256: from memory, so that they stay multiplications (another pipe)
