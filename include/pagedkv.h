@@ -399,7 +399,8 @@ int pa_dequantize_blocks_int4(void *key_out, void *value_out, const void *key_ca
                               int block_size, int num_blocks, void *stream);
 
 /* Single-query paged decode over a 4-bit cache: the result of pa_decode with K
- * and V the values the codes stand for (G = num_heads / num_kv_heads in 1..16).
+ * and V the values the codes stand for (G = num_heads / num_kv_heads in 1..16;
+ * scale finite).
  * The work is split over the GPU by the lengths found on the device, so no
  * bound of the lengths is passed; one launch.  A length of 0 or less gives
  * zeros, a length past max_blocks_per_seq * block_size counts as that.  A table
@@ -477,7 +478,8 @@ int pa_qk_norm_rope_cache_int4(void *query_out, const void *query, const void *k
  * requests' lengths: the counterpart of pa_pool_prepare_decode for batches
  * whose lengths never leave the GPU (prompt chunks and decodes mixed).  The free
  * blocks are a stack in device memory, handed out from its end; blocks have one
- * owner (sharing and copy-on-write stay with the host pool).
+ * owner (sharing and copy-on-write stay with the host pool), so the entries of the
+ * stack and of the tables in use are distinct.
  *   context_lens, query_lens: int32 [num_seqs], cached and new tokens;
  *   free_blocks: int32 [free_capacity]; num_free: int32 [1], how many are free.
  * With have = ceil(context / block_size), need = ceil((context + new) /

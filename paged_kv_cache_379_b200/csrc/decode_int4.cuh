@@ -26,7 +26,7 @@
 // query heads on each of 8 KV heads (160 MB) 42 us, 64 sequences with 32 heads (323
 // MB) 69 us: 26 and 51 us of stages, 4 of start, the rest the join, where the SMs
 // wait for their last warps and for cold code.  A stage takes about 440
-// instructions; the pipe of the ANDs is the fullest (57 %).
+// instructions: 58 % of the issue slots, 49 % of the pipe of the ANDs.
 // Included once, by pagedkv.cu.
 #pragma once
 
@@ -731,21 +731,25 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     float *const wf = reinterpret_cast<float *>(smem + Lay::kQf);  // [part][head]: the queries are done with
     constexpr int H = 8 * NG;
     auto run_of = [&](int e) {  // the parts of e's run
-        const int b = 31 - __clz(begins & (2u << e) - 1);
+        const int b = 31 - __clz(begins & ((2u << e) - 1));
         const unsigned after = begins & ~((2u << e) - 1);
         return parts & ~((1u << b) - 1) & (after ? (after & -after) - 1 : ~0u);
     };
-    if (tid < 2 * W * H && (parts >> tid / H & 1u)) {
+    if (tid < 2 * W * H && ((parts >> (tid / H)) & 1u)) {
         const int e = tid / H, hd = tid % H;
         const float fq = s_cut[e >> 1][e & 1].qa[hd];
         const unsigned run = run_of(e);
         float M = -INFINITY, L = 0.f;
-        for (unsigned b = run; b; b &= b - 1) M = fmaxf(M, s_cut[__ffs(b) - 1 >> 1][__ffs(b) - 1 & 1].m[hd]);
         for (unsigned b = run; b; b &= b - 1) {
-            const Int4Cut<NG> &u = s_cut[__ffs(b) - 1 >> 1][__ffs(b) - 1 & 1];
+            const int x = __ffs(b) - 1;
+            M = fmaxf(M, s_cut[x >> 1][x & 1].m[hd]);
+        }
+        for (unsigned b = run; b; b &= b - 1) {
+            const int x = __ffs(b) - 1;
+            const Int4Cut<NG> &u = s_cut[x >> 1][x & 1];
             const float f = fast_exp2(fq * (u.m[hd] - M));
             L = fmaf(f, u.l[hd], L);
-            if (__ffs(b) - 1 == e) wf[tid] = f;
+            if (x == e) wf[tid] = f;
         }
         wf[2 * W * H + tid] = L;
         wf[4 * W * H + tid] = M;
@@ -753,8 +757,8 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     __syncthreads();
     // A part of the unit shared with earlier / later CTAs, or -1: the first run's, the last one's.
     const int first_part = __ffs(parts) - 1, last_part = 31 - __clz(parts);  // -1: none
-    const int left = have & 1u ? 0 : first_part >= 0 && (from >> first_part & 1u) ? first_part : -1;
-    int right = last_part >= 0 && (to >> last_part & 1u) ? 31 - __clz(begins) : -1;
+    const int left = (have & 1u) ? 0 : first_part >= 0 && ((from >> first_part) & 1u) ? first_part : -1;
+    int right = last_part >= 0 && ((to >> last_part) & 1u) ? 31 - __clz(begins) : -1;
     for (int cell = tid; cell < NG * Lay::kChunks * 32; cell += W * 32) {
         const int k = (cell >> 5) % Lay::kChunks, hd = (cell >> 5) / Lay::kChunks * 8 + 2 * c + k / (MT / 2);
         if (hd >= p.group) continue;
@@ -770,11 +774,11 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             acc.y = fmaf(f, v.y, acc.y);
             acc.z = fmaf(f, v.z, acc.z);
             acc.w = fmaf(f, v.w, acc.w);
-            const bool ends = !b || (begins >> (__ffs(b) - 1) & 1u);
+            const bool ends = !b || ((begins >> (__ffs(b) - 1)) & 1u);
             if (!ends) continue;
             // the run's last part: out it goes
             const float L = wf[2 * W * H + e * H + hd];
-            const int b0 = 31 - __clz(begins & (2u << e) - 1);
+            const int b0 = 31 - __clz(begins & ((2u << e) - 1));
             if (b0 != left && b0 != right) {
                 const Int4Cut<NG> &u = s_cut[e >> 1][e & 1];
                 const float inv = 1.f / L;
@@ -798,7 +802,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         const int e = warp ? right : left;
         if (e >= 0) {
             const Int4Cut<NG> &u = s_cut[e >> 1][e & 1];
-            const int first = from >> e & 1u ? int4_cta_of(s_split, u.unit + kI4UnitCost) : blockIdx.x;
+            const int first = ((from >> e) & 1u) ? int4_cta_of(s_split, u.unit + kI4UnitCost) : blockIdx.x;
             const int last = int4_cta_of(s_split, u.unit + kI4UnitCost + u.nt - 1);
             const int n = last - first;  // arrivals before the last one
             __threadfence();  // the CTA's part, behind the barrier above

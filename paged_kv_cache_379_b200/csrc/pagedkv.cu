@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <mutex>
 #include <tuple>
 #include <vector>
@@ -1284,7 +1285,8 @@ int pa_decode_int4(void *out, const void *query, const void *key_cache, const vo
                    int num_kv_heads, int num_seqs, int num_heads, int head_dim, int max_blocks_per_seq,
                    int num_blocks, void *workspace, size_t workspace_bytes, void *stream)
 {
-    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0) return PA_ERR_BAD_SHAPE;
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 || !(std::fabs(scale) < INFINITY))
+        return PA_ERR_BAD_SHAPE;
     if (num_heads % num_kv_heads != 0) return PA_ERR_BAD_SHAPE;
     if (num_heads / num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
     const int rc = check_int4_cache(key_cache, value_cache, num_kv_heads, head_dim, block_size, num_blocks);

@@ -666,8 +666,8 @@ def prepare_batch(block_tables, context_lens, query_lens, free_blocks, num_free,
         _arr(dev, seq_lens, i32, "seq_lens", 1, B), _arr(dev, q_start, i32, "q_start", 1, B + 1),
         _opt(dev, seq_ids, i32, "seq_ids", n), _opt(dev, positions, i64, "positions", n),
         _opt(dev, slot_mapping, i64, "slot_mapping", n), _arr(dev, num_free_out, i32, "num_free_out", 1, 1),
-        _arr(dev, status, i32, "status", 1, 1), B, block_tables.size(1), n, free_blocks.size(0), block_size,
-        num_blocks, _raw_stream(stream, dev)))
+        _arr(dev, status, i32, "status", 1, 1), B, block_tables.size(1), int(n), free_blocks.size(0),
+        int(block_size), int(num_blocks), _raw_stream(stream, dev)))
 
 
 def release_blocks(block_tables, seq_lens, release, free_blocks, num_free, block_size: int, num_blocks: int, *,
@@ -680,7 +680,7 @@ def release_blocks(block_tables, seq_lens, release, free_blocks, num_free, block
     check("pa_release_blocks", load().pa_release_blocks(
         bt, _arr(dev, seq_lens, i32, "seq_lens", 1, B), _arr(dev, release, i32, "release", 1, B),
         _arr(dev, free_blocks, i32, "free_blocks", 1), _arr(dev, num_free, i32, "num_free", 1, 1),
-        _arr(dev, status, i32, "status", 1, 1), B, block_tables.size(1), free_blocks.size(0), block_size, num_blocks,
+        _arr(dev, status, i32, "status", 1, 1), B, block_tables.size(1), free_blocks.size(0), int(block_size), int(num_blocks),
         _raw_stream(stream, dev)))
 
 

@@ -208,7 +208,7 @@ def test_decode_one_long_sequence(G, H, L):
     _check(f"int4 decode one {L} G{G} H{H}", out, want, bound)
 
 
-@pytest.mark.parametrize("B", [130, 700])
+@pytest.mark.parametrize("B", [130, 700, 2500])
 def test_decode_many_sequences(B):
     """More sequences than threads of a CTA; most lengths short, some zero."""
     rng = np.random.default_rng(B)
@@ -217,6 +217,26 @@ def test_decode_many_sequences(B):
     q, kc, vc, tables, ln = _problem(lens.tolist(), 4, 2, 64, 16, seed=B)
     want, bound = ref.decode(q, kc, vc, tables, ln, 0.125, 16)
     _check(f"int4 decode {B} seqs", _run(q, kc, vc, tables, ln, 0.125), want, bound)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_decode_random_mixes(seed):
+    """Lengths from none to thousands in one batch, so that units are cut between warps and between CTAs in every way."""
+    rng = np.random.default_rng(1000 + seed)
+    D, bs = int(rng.choice([64, 128])), int(rng.choice([8, 16, 32]))
+    H, G = int(rng.integers(1, 6)), int(rng.choice([1, 2, 3, 4, 6, 8, 11, 16]))
+    lens = np.exp(rng.uniform(0, np.log(6000), int(rng.integers(1, 40)))).astype(int) - 1
+    q, kc, vc, tables, ln = _problem(lens.tolist(), G * H, H, D, bs, seed=seed)
+    want, bound = ref.decode(q, kc, vc, tables, ln, 0.1, bs)
+    _check(f"int4 decode mix {seed}: D{D} bs{bs} H{H} G{G}", _run(q, kc, vc, tables, ln, 0.1), want, bound)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.09, 1e-30, 3.0])
+def test_decode_scales(scale):
+    """No, negative, vanishing and large softmax scales."""
+    q, kc, vc, tables, ln = _problem([1, 40, 333, 700], 8, 2, 128, 16, seed=17)
+    want, bound = ref.decode(q, kc, vc, tables, ln, scale, 16)
+    _check(f"int4 decode scale {scale:g}", _run(q, kc, vc, tables, ln, scale), want, bound)
 
 
 def test_decode_all_empty():

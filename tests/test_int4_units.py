@@ -82,6 +82,8 @@ def test_decode_argument_errors(lib):
     assert call(hq=63) == -2
     assert call(hq=136) == -3              # 17 query heads per KV head
     assert call(b=-1) == -2
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        assert call(scale=bad) == -2
     assert call(b=65536) == -2
     assert call(mb=0) == -2
     assert call(mb=1 << 28) == -2
