@@ -63,7 +63,9 @@ struct Int4Lay {
     static constexpr int kRing = kSlots * kStage;
     static constexpr int kChunks = D / 16;                     // float4s a lane holds of 8 heads
     static constexpr int kPart = NG * kChunks * 512;           // bytes of a warp's result
-    static constexpr int kCtas = NG == 1 ? 4 : 3;              // resident CTAs per SM
+    // resident CTAs per SM: what registers and shared memory hold (64 sequences with 16 heads on each of 8 KV heads:
+    // 50 us with two, 79 with registers for a third that does not fit)
+    static constexpr int kCtas = NG == 1 ? 4 : D == 64 ? 3 : 2;
     static constexpr int kQf = kI4Warps * kRing;               // each warp's queries as operands
     static constexpr int kQfBytes = NG * (D / 32) * 512;
     static constexpr int kHead = kQf + kI4Warps * kQfBytes;    // results of the first units of warps 1, 2, 3
@@ -176,6 +178,7 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 // the place that falls free: eight long sequences 142 instead of 134 us.)
 struct Int4Split {
     int64_t each, rest;
+    float cta;  // a CTA's share, about
 };
 
 __device__ __forceinline__ int64_t int4_begin(const Int4Split &x, int worker)
@@ -183,10 +186,10 @@ __device__ __forceinline__ int64_t int4_begin(const Int4Split &x, int worker)
     return worker * x.each + min((int64_t)worker, x.rest);
 }
 
-// The CTA that holds position x of `total`: a guess in floating point, then the exact one.
+// The CTA that holds position x: a guess in floating point, then the exact one.
 __device__ __forceinline__ int int4_cta_of(const Int4Split &s, int64_t x)
 {
-    int cta = min((int)((float)x / ((float)s.each * kI4Warps)), (int)gridDim.x - 1);
+    int cta = min((int)((float)x / s.cta), (int)gridDim.x - 1);
     while (int4_begin(s, cta * kI4Warps) > x) --cta;
     while (cta + 1 < (int)gridDim.x && int4_begin(s, (cta + 1) * kI4Warps) <= x) ++cta;
     return cta;
@@ -248,6 +251,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         split.each = total / workers;
     }
     split.rest = total - split.each * workers;
+    split.cta = (float)total / (float)workers * W;
     for (int w = 0; w < W; ++w) {  // whose sequence is in here?
         const int id = blockIdx.x * W + w;
         const int64_t lo = int4_begin(split, id);
@@ -821,57 +825,77 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         const Int4Cut<NG> *u = &s_cut[e >> 1][e & 1];
         const int first = s_first[side], last = s_end[side];
         const int items = p.group * (D / 4);
-        // a thread per 4 dims of a head; where those are fewer than the threads, `ways` of
-        // them share the parts.  U parts are in flight at a time.
-        constexpr int U = 4;
+        // 4 dims of a head a thread and item; where those are fewer than the threads, `ways` of
+        // them share the parts.  U parts of every item are in flight at a time.
+        constexpr int U = 4, ITS = NG * D / 64;
         const int ways = items < W * 32 ? W * 32 / items : 1;
-        const int way = ways > 1 ? tid / items : 0;
+        const int way = tid / items;  // from `ways` on: nothing to do
+        const int it0 = tid - way * items;
         uint8_t *const join = smem + side * Lay::kRing;  // rings are free
-        for (int it = ways > 1 ? tid - way * items : tid; it < items && way < ways; it += W * 32) {
-            const int hd = it / (D / 4), d4 = it % (D / 4);
-            const int cell = ((hd >> 3) * Lay::kChunks + (hd & 1) * (D / 32) + d4 / 8) * 32 + d4 % 8 * 4 + ((hd & 7) >> 1);
-            const float fq = u->qa[hd];
-            float M = -INFINITY, L = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = first + way; w <= last; w += ways * U) {
-                float2 ml[U];
-                float4 r[U];
+        float M[ITS], L[ITS];
+        float4 sums[ITS];
+#pragma unroll
+        for (int i = 0; i < ITS; ++i) {
+            M[i] = -INFINITY;
+            L[i] = 0.f;
+            sums[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int w = way < ways ? first + way : last + 1; w <= last; w += ways * U) {
+            float2 ml[ITS][U];
+            float4 r[ITS][U];
+#pragma unroll
+            for (int i = 0; i < ITS; ++i)
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
+                    const int it = it0 + i * W * 32, hd = it / (D / 4), d4 = it % (D / 4);
                     const int x = w + u * ways;
                     const int64_t q = 2 * x + (x == first ? 1 : 0);
-                    ml[u] = make_float2(-INFINITY, 0.f);
-                    r[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (x <= last) {
-                        ml[u] = __ldcg(&p.part_ml[q * 16 + hd]);
-                        r[u] = __ldcg(&p.part_o[q * (NG * Lay::kChunks * 32) + cell]);
+                    ml[i][u] = make_float2(-INFINITY, 0.f);
+                    r[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (x <= last && it < items) {
+                        ml[i][u] = __ldcg(&p.part_ml[q * 16 + hd]);
+                        r[i][u] = __ldcg(&p.part_o[q * (NG * Lay::kChunks * 32) + ((hd >> 3) * Lay::kChunks +
+                                                   (hd & 1) * (D / 32) + d4 / 8) * 32 + d4 % 8 * 4 + ((hd & 7) >> 1)]);
                     }
                 }
-                float to = M;
 #pragma unroll
-                for (int u = 0; u < U; ++u) to = fmaxf(to, ml[u].x);
-                const float corr = M == -INFINITY ? 0.f : exp2f(fq * (M - to));
-                M = to;
-                L *= corr;
+            for (int i = 0; i < ITS; ++i) {
+                const int it = it0 + i * W * 32;
+                if (it >= items) break;
+                const float fq = u->qa[it / (D / 4)];
+                float to = M[i];
+#pragma unroll
+                for (int u = 0; u < U; ++u) to = fmaxf(to, ml[i][u].x);
+                const float corr = M[i] == -INFINITY ? 0.f : fast_exp2(fq * (M[i] - to));
+                float4 &acc = sums[i];
+                M[i] = to;
+                L[i] *= corr;
                 acc.x *= corr, acc.y *= corr, acc.z *= corr, acc.w *= corr;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const float f = fast_exp2(fq * (ml[u].x - M));
-                    L = fmaf(f, ml[u].y, L);
-                    acc.x = fmaf(f, r[u].x, acc.x);
-                    acc.y = fmaf(f, r[u].y, acc.y);
-                    acc.z = fmaf(f, r[u].z, acc.z);
-                    acc.w = fmaf(f, r[u].w, acc.w);
+                    const float f = fast_exp2(fq * (ml[i][u].x - to));
+                    L[i] = fmaf(f, ml[i][u].y, L[i]);
+                    acc.x = fmaf(f, r[i][u].x, acc.x);
+                    acc.y = fmaf(f, r[i][u].y, acc.y);
+                    acc.z = fmaf(f, r[i][u].z, acc.z);
+                    acc.w = fmaf(f, r[i][u].w, acc.w);
                 }
             }
-            if (ways > 1) {
-                *reinterpret_cast<float4 *>(join + tid * 16) = acc;
-                if (d4 == 0) *reinterpret_cast<float2 *>(join + W * 32 * 16 + tid / (D / 4) * 8) = make_float2(M, L);
-            } else {
-                const float inv = 1.f / L;
-                *reinterpret_cast<uint2 *>(
-                    p.out + ((int64_t)u->s * p.num_heads + u->h * p.group + hd) * D + 4 * d4) =
-                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        }
+        if (ways > 1) {
+            if (way < ways) {
+                *reinterpret_cast<float4 *>(join + tid * 16) = sums[0];
+                if (tid % (D / 4) == 0)
+                    *reinterpret_cast<float2 *>(join + W * 32 * 16 + tid / (D / 4) * 8) = make_float2(M[0], L[0]);
+            }
+        } else if (way == 0) {
+#pragma unroll
+            for (int i = 0; i < ITS; ++i) {
+                const int it = it0 + i * W * 32;
+                if (it >= items) break;
+                const float inv = 1.f / L[i];
+                *reinterpret_cast<uint2 *>(p.out + ((int64_t)u->s * p.num_heads + u->h * p.group) * D + 4 * it) =
+                    make_uint2(pack_bf16x2(sums[i].x * inv, sums[i].y * inv), pack_bf16x2(sums[i].z * inv, sums[i].w * inv));
             }
         }
         if (ways > 1) {

@@ -510,7 +510,7 @@ static int write_int4(const void *key, const void *value, int64_t key_stride, in
 
 // 4-bit decode workspace: arrival counters, (m, l) and the results of two cut
 // units per CTA.  Groups of more than 8 query heads hold twice the result and
-// run 3 instead of 4 CTAs per SM.
+// run at most 3 instead of 4 CTAs per SM.
 struct Int4Workspace {
     int ctas;
     size_t part_o, bytes;
