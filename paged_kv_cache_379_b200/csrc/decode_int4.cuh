@@ -21,8 +21,8 @@
 // for the grouped-query batch, 8.7 instead of 3.8 for four short sequences.)
 //
 // Bound, head_dim 128 and block_size 16, one launch after another: eight sequences of
-// 32K-128K tokens (713 MB) 131 us, 83 % of the measured copy rate, its stages at that
-// rate and the rest the start (4 us) and the join; 128 sequences of ~1100 tokens, 8
+// 32K-128K tokens (713 MB) 131 to 138 us from GPU to GPU, 80 to 83 % of the measured
+// copy rate, its stages near that rate and the rest the start (4 us) and the join; 128 sequences of ~1100 tokens, 8
 // query heads on each of 8 KV heads (160 MB) 42 us, 64 sequences with 32 heads (323
 // MB) 69 us: 26 and 51 us of stages, 4 of start, the rest the join, where the SMs
 // wait for their last warps and for cold code.  A stage takes about 440

@@ -384,6 +384,9 @@ def decode_shared(query, key_cache, value_cache, block_tables, seq_lens, scale: 
 # The calls below are made once per layer and step, where the time of the marshalling itself counts: they ask
 # each tensor for as little as the checks need (get_device, dim and size answer without building objects).
 
+_current_device = torch._C._cuda_getDevice  # torch.cuda.current_device() without its check for a first use
+
+
 def _device(t, name: str) -> int:
     """The device of a call's first tensor: the library launches on the current one, so it has to be that."""
     if not isinstance(t, torch.Tensor):
@@ -391,8 +394,8 @@ def _device(t, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{_current_device()}")
     return dev
 
 
@@ -467,9 +470,10 @@ def _int4_caches(dev: int, key_cache, value_cache, head_dim: int):
     """(key pointer, value pointer, num_blocks, block_size, num_kv_heads) of two 4-bit caches."""
     kc = _arr(dev, key_cache, torch.uint8, "key_cache", 3)
     vc = _arr(dev, value_cache, torch.uint8, "value_cache", 3)
-    nb, hkv, rec = key_cache.shape
-    if value_cache.shape != key_cache.shape:
+    shape = key_cache.shape
+    if value_cache.shape != shape:
         raise ValueError("key_cache and value_cache shapes differ")
+    nb, hkv, rec = shape
     row = head_dim // 2 + 4
     if head_dim <= 0 or rec % row != 0:
         raise ValueError(f"cache records of {rec} bytes do not hold rows of head_dim {head_dim}")
@@ -539,15 +543,16 @@ def decode_int4(query, key_cache, value_cache, block_tables, seq_lens, scale: fl
                 stream=None):
     """pa_decode_int4: single-query paged decode over 4-bit caches."""
     dev = _device(query, "query")
-    B, hq, d = _dims3(query, "query")
     q = _arr(dev, query, torch.bfloat16, "query", 3)
+    shape = query.shape
+    B, hq, d = shape
     kc, vc, nb, bs, hkv = _int4_caches(dev, key_cache, value_cache, d)
     bt = _arr(dev, block_tables, torch.int32, "block_tables", 2, B)
     sl = _arr(dev, seq_lens, torch.int32, "seq_lens", 1, B)
     if out is None:
         out = torch.empty_like(query)
     o = _arr(dev, out, torch.bfloat16, "out", 3, B)
-    if out.shape != query.shape:
+    if out.shape != shape:
         raise ValueError("out must have the query's shape")
     if workspace is None:
         wp, wb = None, 0

@@ -181,12 +181,12 @@ def test_binding_refuses_another_device(monkeypatch):
         def get_device(self):
             return 1
     t = torch.zeros(1).as_subclass(Fake)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(ops, "_current_device", lambda: 0)
     with pytest.raises(ValueError, match="current device is cuda:0"):
         ops._device(t, "query")
     with pytest.raises(ValueError, match="not on cuda:0"):
         ops._arr(0, t, torch.float32, "out", 1)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(ops, "_current_device", lambda: 1)
     assert ops._device(t, "query") == 1
     assert ops._arr(1, t, torch.float32, "out", 1, 1) == t.data_ptr()
 
