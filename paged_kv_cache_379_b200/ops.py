@@ -455,6 +455,18 @@ def _raw_stream(stream, dev: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _output(make, shape, device, stream):
+    """A call's default output (bf16), allocated and filled in the order of the stream that the call runs on: on
+    another one, its fill, or what the allocator's last user of that memory still has in flight, could land on top
+    of the result."""
+    if stream is None:
+        return make(shape, dtype=torch.bfloat16, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_raw_stream(stream, device.index), device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=torch.bfloat16, device=device)
+
+
 def int4_record_bytes(block_size: int, head_dim: int) -> int:
     """Bytes of one (block, KV head) record of a 4-bit cache."""
     return int(block_size) * (int(head_dim) // 2 + 4)
@@ -515,9 +527,9 @@ def dequantize_blocks_int4(key_cache, value_cache, block_ids, head_dim: int, *, 
     ids = _arr(dev, block_ids, torch.int32, "block_ids", 1)
     n = block_ids.size(0)
     if key_out is None:
-        key_out = torch.zeros((n, bs, hkv, d), dtype=torch.bfloat16, device=key_cache.device)
+        key_out = _output(torch.zeros, (n, bs, hkv, d), key_cache.device, stream)
     if value_out is None:
-        value_out = torch.zeros((n, bs, hkv, d), dtype=torch.bfloat16, device=key_cache.device)
+        value_out = _output(torch.zeros, (n, bs, hkv, d), key_cache.device, stream)
     ko = _arr(dev, key_out, torch.bfloat16, "key_out", 4, n)
     vo = _arr(dev, value_out, torch.bfloat16, "value_out", 4, n)
     shape = (n, bs, hkv, d)
@@ -550,7 +562,7 @@ def decode_int4(query, key_cache, value_cache, block_tables, seq_lens, scale: fl
     bt = _arr(dev, block_tables, torch.int32, "block_tables", 2, B)
     sl = _arr(dev, seq_lens, torch.int32, "seq_lens", 1, B)
     if out is None:
-        out = torch.empty_like(query)
+        out = _output(torch.empty, shape, query.device, stream)
     o = _arr(dev, out, torch.bfloat16, "out", 3, B)
     if out.shape != shape:
         raise ValueError("out must have the query's shape")
@@ -569,7 +581,7 @@ def decode_int4(query, key_cache, value_cache, block_tables, seq_lens, scale: fl
 
 # ---- head norm + rotation -------------------------------------------------------------
 
-def _rope_args(query, key, q_weight, k_weight, cos_sin, positions, query_out):
+def _rope_args(query, key, q_weight, k_weight, cos_sin, positions, query_out, stream):
     """What the rotation calls share: the device, the sizes, and the leading pointers."""
     dev = _device(query, "query")
     T, hq, d = _dims3(query, "query")
@@ -581,7 +593,7 @@ def _rope_args(query, key, q_weight, k_weight, cos_sin, positions, query_out):
     cs = _arr(dev, cos_sin, torch.float32, "cos_sin", 2)
     ps = _arr(dev, positions, torch.int64, "positions", 1, T)
     if query_out is None:
-        query_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=query.device)
+        query_out = _output(torch.empty, (T, hq, d), query.device, stream)
     qo, qos = _rows(dev, query_out, "query_out", T, hq, d)
     return dev, T, hq, hkv, d, query_out, qo, qos, q, qs, k, ks, (qw, kw, cs, ps)
 
@@ -590,9 +602,9 @@ def qk_norm_rope(query, key, q_weight, k_weight, cos_sin, positions, *, eps: flo
                  query_out=None, key_out=None, stream=None):
     """pa_qk_norm_rope: RMS norm of every query and key head and position rotation.  Returns (query_out, key_out)."""
     dev, T, hq, hkv, d, query_out, qo, qos, q, qs, k, ks, rest = _rope_args(query, key, q_weight, k_weight, cos_sin,
-                                                                            positions, query_out)
+                                                                            positions, query_out, stream)
     if key_out is None:
-        key_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=key.device)
+        key_out = _output(torch.empty, (T, hkv, d), key.device, stream)
     ko, kos = _rows(dev, key_out, "key_out", T, hkv, d)
     check("pa_qk_norm_rope", load().pa_qk_norm_rope(
         qo, ko, q, k, *rest, float(eps), qos, kos, qs, ks, cos_sin.size(1), 1 if interleaved else 0, cos_sin.size(0),
@@ -603,7 +615,7 @@ def qk_norm_rope(query, key, q_weight, k_weight, cos_sin, positions, *, eps: flo
 def _rope_cache(name, extra, query, key, value, q_weight, k_weight, cos_sin, positions, slot_mapping, key_cache,
                 value_cache, eps, interleaved, query_out, stream):
     dev, T, hq, hkv, d, query_out, qo, qos, q, qs, k, ks, rest = _rope_args(query, key, q_weight, k_weight, cos_sin,
-                                                                            positions, query_out)
+                                                                            positions, query_out, stream)
     v, vs = _rows(dev, value, "value", T, hkv, d)
     if name == "pa_qk_norm_rope_cache_int4":
         kc, vc, nb, bs, heads = _int4_caches(dev, key_cache, value_cache, d)
