@@ -384,7 +384,11 @@ def decode_shared(query, key_cache, value_cache, block_tables, seq_lens, scale: 
 # The calls below are made once per layer and step, where the time of the marshalling itself counts: they ask
 # each tensor for as little as the checks need (get_device, dim and size answer without building objects).
 
-_current_device = torch._C._cuda_getDevice  # torch.cuda.current_device() without its check for a first use
+# torch.cuda.current_device() without its check for a first use, and current_stream(dev).cuda_stream without the
+# objects; a torch built without CUDA has neither name
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _device(t, name: str) -> int:
@@ -451,7 +455,7 @@ def _dims3(t, name: str):
 
 def _raw_stream(stream, dev: int) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)  # current_stream(dev).cuda_stream without the objects
+        return _current_raw_stream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
