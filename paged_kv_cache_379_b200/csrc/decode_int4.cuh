@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
 
             // ---- running maximum and value scale, moved only when a logit passes the
             // maximum by more than 4 (so a weight stays below 2^4) or a scale its bound
-            const float vtop = fmaxf(fmaxf(vp[0].x, vp[1].x), fmaxf(vp[2].x, vp[3].x));
+            const float vtop = fmaxf(fmaxf(fabsf(vp[0].x), fabsf(vp[1].x)), fmaxf(fabsf(vp[2].x), fabsf(vp[3].x)));
             float top[NG][2];
             bool move = vtop * vmul >= 2048.f;
 #pragma unroll
