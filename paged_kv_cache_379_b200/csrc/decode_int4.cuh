@@ -4,11 +4,13 @@
 //     x_t = scale * (s_t (q . c_t) + z_t sum(q)),   p_t = 2^(x_t log2 e - m),
 //     out = (sum_t (p_t s'_t) c'_t + sum_t p_t z'_t) / sum_t p_t,
 // so a row's scale and zero meet its codes only in per-token scalars, and the
-// codes go to the tensor cores as they are.  Key product: a word's low nibbles, and
-// its high nibbles in place (16 c), are unsigned bytes after one AND each; the query
-// is an integer of 16 bits in two bytes.  Value product: a nibble in bits 0-3 of a
-// half word is the fp16 subnormal c 2^-24, one in bits 4-7 is 16 c 2^-24, so one AND
-// gives two exact operands, and the 16 comes out of the accumulator.
+// codes go to the tensor cores as they are: a nibble in bits 0-3 of a half word is
+// the fp16 subnormal c 2^-24, one in bits 4-7 is 16 c 2^-24, so one AND gives two
+// exact operands.  In the key product the 16 goes into the query, which is exact in
+// fp16 (as a 16-bit integer on the byte product 42.0 instead of 44.6 us for the
+// grouped-query batch, but every entry off by up to 2^-15 of a head's largest, times its
+// code: one entry 2^10 times the others cost 2 % of the result); in the value product it
+// comes out of the accumulator.
 //
 // Work: a unit is one sequence and KV head, a stage 32 of its tokens.  The weight of
 // all units is cut into equal ranges, one for each warp of the grid, so a long
@@ -51,7 +53,6 @@ struct Int4DecodeParams {
     float4 *part_o;                     // [2 CTAs][NG * D/16 chunks][32 lanes]
     float scale_log2;                   // scale * log2(e)
     int num_seqs, num_heads, num_kv_heads, group, max_blocks, num_blocks, min_stages;
-    int c16, c256;                      // 16 and 256: from memory, so that they stay multiplications (another pipe)
 };
 
 template <int D, int BS, int NG>
@@ -147,24 +148,6 @@ __device__ __forceinline__ void mma_codes(float *d, uint32_t a0, uint32_t a1, ui
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// D = A(16x32, row, u8) * B(32x8, col) + C in s32; B unsigned, or signed where SGN; C = D, or 0 where ZERO.
-template <bool SGN, bool ZERO>
-__device__ __forceinline__ void mma_bytes(int *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1)
-{
-    if constexpr (ZERO) d[0] = d[1] = d[2] = d[3] = 0;
-    if constexpr (SGN)
-        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%10, %11, %12, %13};"
-            : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]));
-    else
-        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%10, %11, %12, %13};"
-            : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]));
 }
 
 // ev of vmul = 2^(10 - ev)
@@ -403,9 +386,11 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
 
     int slot = 0;
     while (more) {
-        // ---- the unit's queries: 16-bit integers, each head scaled by a power of two (its largest
-        // magnitude into [2^14, 2^15)): exact for entries within 2^8 of that, the others off by at most
-        // half a step.  Bytes of the even dims of words j, j + 1 of a row's lane, then of the odd ones.
+        // ---- the unit's queries as fp16, each head scaled by a power of two: its largest magnitude into
+        // [2^14, 2^15), and 2^-4 of that for the odd dims, whose codes come as 16 c: exact for entries down to
+        // 2^-27 of the largest.  A word's operands lie together.  (A product of a subnormal code is cut 2^-25
+        // below its nominal exponent: at 2^-15 of the largest entry of its 16 dims, for products of up to 15
+        // times an entry.)
         float qa[NG][2], qb[NG][2];
         const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
 #pragma unroll
@@ -429,39 +414,24 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             top2 = max_nan_bf16x2(top2, __shfl_xor_sync(FULL, top2, 2));
             const uint32_t top = max_nan_bf16x2(top2, prmt(top2, top2, 0x1032u)) & 0x7FFFu;
             const int e = max((int)(top >> 7) - 127, -100);
-            const float mul = pow2i(max(14 - e, -126)) * sign;
+            const float even = pow2i(14 - e) * sign, odd = pow2i(10 - e) * sign;
 #pragma unroll
-            for (int j = 0; j < KW; j += 2) {
-                uint32_t hi[2][2], lw[2][2];  // [odd][word]
+            for (int j = 0; j < KW; ++j) {
+                float x[8];
+                unpack8(raw[j], x);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float x[8];
-                    unpack8(raw[j + k], x);
-                    uint32_t v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        sum += x[i];
-                        v[i] = (uint32_t)__float2int_rn(x[i] * mul);
-                    }
-#pragma unroll
-                    for (int odd = 0; odd < 2; ++odd) {
-                        const uint32_t a = prmt(v[odd], v[2 + odd], 0x5140u), b = prmt(v[4 + odd], v[6 + odd], 0x5140u);
-                        lw[odd][k] = prmt(a, b, 0x5410u);
-                        hi[odd][k] = prmt(a, b, 0x7632u);
-                    }
-                }
-#pragma unroll
-                for (int odd = 0; odd < 2; ++odd)
-                    *reinterpret_cast<uint4 *>(qop + ((n * KW + j + odd) * 32 + lane) * 16) =
-                        make_uint4(hi[odd][0], hi[odd][1], lw[odd][0], lw[odd][1]);
+                for (int i = 0; i < 8; ++i) sum += x[i];
+                *reinterpret_cast<uint4 *>(qop + ((n * KW + j) * 32 + lane) * 16) =
+                    make_uint4(pack_f16x2(x[0] * even, x[4] * even), pack_f16x2(x[1] * odd, x[5] * odd),
+                               pack_f16x2(x[2] * even, x[6] * even), pack_f16x2(x[3] * odd, x[7] * odd));
             }
             sum += __shfl_xor_sync(FULL, sum, 1);
             sum += __shfl_xor_sync(FULL, sum, 2);
-            // log2-logit = qa (s S + z qb): S = +-(q . codes) 2^18 2^-e; an infinity or a NaN in the
+            // log2-logit = qa (s S + z qb): S = +-(q . codes) 2^-10 2^-e, below 4; an infinity or a NaN in the
             // query makes it NaN.  qa > 0, so the largest product is the largest logit.
-            const float a = fminf(fmaxf(fabsf(p.scale_log2) * 3.814697265625e-6f * pow2i(min(e, 127)), 1.17549435e-38f), 3.4e38f);
+            const float a = fminf(fmaxf(fabsf(p.scale_log2) * 1024.f * pow2i(min(e, 127)), 1.17549435e-38f), 3.4e38f);
             const float b = top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
-                                           : sum * (sign * 262144.f) * pow2i(-(e >> 1)) * pow2i((e >> 1) - e);
+                                           : sum * (sign * 9.765625e-4f) * pow2i(-(e >> 1)) * pow2i((e >> 1) - e);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 qa[n][i] = __shfl_sync(FULL, a, (2 * c + i) * 4);
@@ -497,48 +467,36 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             const uint8_t *kb = ring + slot * Lay::kStage, *vb = kb + RECS * REC;
             const uint32_t vb32 = smem_u32(vb);
 
-            // ---- S = 16 codes . q: 16 tokens x 8 heads x 32 dims a step; the four sums (low or high
-            // nibbles) x (high or low byte of the query) are joined as integers below 2^31
+            // ---- S = codes . q: 16 tokens x 8 heads x 16 dims a step, the stage's two token tiles in turn
             float sc[2][NG][4];
+            uint32_t kw[2][2][KW];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-                uint32_t kw[2][KW];
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const uint8_t *a = kb + row_at(2 * mt + hf, g) + c * (D / 8);
                     if constexpr (KW == 4) {
                         const uint4 u = *reinterpret_cast<const uint4 *>(a);
-                        kw[hf][0] = u.x, kw[hf][1] = u.y, kw[hf][2] = u.z, kw[hf][3] = u.w;
+                        kw[mt][hf][0] = u.x, kw[mt][hf][1] = u.y, kw[mt][hf][2] = u.z, kw[mt][hf][3] = u.w;
                     } else {
                         const uint2 u = *reinterpret_cast<const uint2 *>(a);
-                        kw[hf][0] = u.x, kw[hf][1] = u.y;
+                        kw[mt][hf][0] = u.x, kw[mt][hf][1] = u.y;
                     }
                 }
 #pragma unroll
+            for (int j = 0; j < KW; ++j)
+#pragma unroll
                 for (int n = 0; n < NG; ++n) {
-                    int s4[2][2][4];  // [nibble][byte]
+                    const uint4 qf = *reinterpret_cast<const uint4 *>(qop + ((n * KW + j) * 32 + lane) * 16);
 #pragma unroll
-                    for (int j = 0; j < KW; j += 2)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t mask = h ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
-                            const uint4 qf = *reinterpret_cast<const uint4 *>(qop + ((n * KW + j + h) * 32 + lane) * 16);
-                            const uint32_t a0 = kw[0][j] & mask, a1 = kw[1][j] & mask, a2 = kw[0][j + 1] & mask,
-                                           a3 = kw[1][j + 1] & mask;
-                            if (j == 0) {
-                                mma_bytes<true, true>(s4[h][0], a0, a1, a2, a3, qf.x, qf.y);
-                                mma_bytes<false, true>(s4[h][1], a0, a1, a2, a3, qf.z, qf.w);
-                            } else {
-                                mma_bytes<true, false>(s4[h][0], a0, a1, a2, a3, qf.x, qf.y);
-                                mma_bytes<false, false>(s4[h][1], a0, a1, a2, a3, qf.z, qf.w);
-                            }
-                        }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sc[mt][n][e] = __int2float_rn((s4[0][0][e] * p.c16 + s4[1][0][e]) * p.c256 +
-                                                      (s4[0][1][e] * p.c16 + s4[1][1][e]));
+                    for (int mt = 0; mt < 2; ++mt) {
+                        const uint32_t x = kw[mt][0][j], y = kw[mt][1][j], x8 = x >> 8, y8 = y >> 8;
+                        if (j == 0) sc[mt][n][0] = sc[mt][n][1] = sc[mt][n][2] = sc[mt][n][3] = 0.f;
+                        mma_codes(sc[mt][n], x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u, qf.x, qf.y);
+                        mma_codes(sc[mt][n], x8 & 0x000F000Fu, y8 & 0x000F000Fu, x8 & 0x00F000F0u, y8 & 0x00F000F0u, qf.z,
+                                  qf.w);
+                    }
                 }
-            }
 
             // ---- logits / qa and the rows' pairs; row g + 8 half of tile mt is token 8 (2 mt + half) + g
             float2 vp[4];

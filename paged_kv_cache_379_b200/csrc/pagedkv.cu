@@ -1316,8 +1316,6 @@ int pa_decode_int4(void *out, const void *query, const void *key_cache, const vo
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = num_blocks;
     p.min_stages = kI4MinStages;
-    p.c16 = 16;
-    p.c256 = 256;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return head_dim == 64 ? launch_decode_int4_d<64>(block_size, p, lay.ctas, st)
                           : launch_decode_int4_d<128>(block_size, p, lay.ctas, st);
