@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             }
         }
 
-        float o[NG][MT][4], m[NG][2], mlim[NG][2], l[NG][2], zs[NG][2];  // m, mlim: in units of qa
+        float o[NG][MT][4], o1[NG][4], m[NG][2], mlim[NG][2], l[NG][2], zs[NG][2];  // m, mlim: in units of qa
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
 #pragma unroll
@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 m[n][i] = mlim[n][i] = -INFINITY;
+                o1[n][i] = o1[n][2 + i] = 0.f;
                 l[n][i] = zs[n][i] = 0.f;
             }
         }
@@ -553,6 +554,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                         l[n][i] *= corr;  // a NaN stays one
                         zs[n][i] *= corr;
                         const float oc = corr * vcorr;
+                        o1[n][i] *= oc;
 #pragma unroll
                         for (int k = 0; k < MT; ++k) {
                             o[n][k][i] *= oc;
@@ -562,11 +564,18 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             }
 
             // ---- weights: fp32 into l and the zeros' sum; times the value scale and rounded
-            // to fp16 (2^-11 relative) for the tensor cores, one 8x8 transpose each
+            // to fp16 (2^-11 relative) for the tensor cores, one 8x8 transpose each.  Codes count from
+            // 7.5: w c = w (c - 7.5) + 7.5 w, and what 7.5 times the rounded weights adds is taken out by
+            // their sum (o1, a row of 2^-10: a normal number, whose products are not cut, see the queries),
+            // while 7.5 times the unrounded ones goes into the zeros' sum.
+            // Counted from 0, the codes' mean would cancel against the zeros and leave 2.9 times the
+            // rounding.  The second tile takes 15 - c with negative weights: both its and the first
+            // tile's accumulators stay near zero, where the tensor cores' truncation of long sums is small
+            // (results of eight long sequences against the fp32 form's: 0.0025 off before, 0.0009 now).
             uint32_t pf[NG][4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float vs = vp[q].x * vmul;
+                const float vs = q < 2 ? vp[q].x * vmul : vp[q].x * -vmul, z = fmaf(7.5f, vp[q].x, vp[q].y);
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
                     float w[2];
@@ -574,7 +583,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                     for (int i = 0; i < 2; ++i) {
                         const float pr = fast_exp2(qa[n][i] * (sc[q >> 1][n][(q & 1) * 2 + i] - m[n][i]));
                         l[n][i] += pr;
-                        zs[n][i] = fmaf(pr, vp[q].y, zs[n][i]);
+                        zs[n][i] = fmaf(pr, z, zs[n][i]);
                         w[i] = pr * vs;
                     }
                     pf[n][q] = movmatrix_trans(pack_f16x2(w[0], w[1]));
@@ -585,13 +594,18 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
+                for (int n = 0; n < NG; ++n)
+                    mma_codes(o1[n], 0x14001400u, 0u, 0x14001400u, 0u, pf[n][2 * mt], pf[n][2 * mt + 1]);
+#pragma unroll
                 for (int x2 = 0; x2 < VW; ++x2) {
                     // [chunk][half] of 8 tokens x 8 half words: a lane gets half word g of tokens 2c, 2c + 1
                     uint32_t v[2][2];
                     ldsm_x4_trans(vb32 + row_at(2 * mt, 0) + vlane[x2], v[0][0], v[0][1], v[1][0], v[1][1]);
 #pragma unroll
                     for (int hw = 0; hw < 2; ++hw) {
-                        const uint32_t x = v[hw][0], y = v[hw][1], x8 = x >> 8, y8 = y >> 8;
+                        const uint32_t flip = mt ? ~0u : 0u;  // 15 - c
+                        const uint32_t x = v[hw][0] ^ flip, y = v[hw][1] ^ flip, x8 = (v[hw][0] >> 8) ^ flip,
+                                       y8 = (v[hw][1] >> 8) ^ flip;
 #pragma unroll
                         for (int n = 0; n < NG; ++n) {
                             mma_codes(o[n][4 * x2 + 2 * hw], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu,
@@ -650,6 +664,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                     l[n][i] += __shfl_xor_sync(FULL, l[n][i], off);
                     zs[n][i] += __shfl_xor_sync(FULL, zs[n][i], off);
                 }
+                zs[n][i] = fmaf(o1[n][i] * -7.5f, f, zs[n][i]);
                 if (poison) l[n][i] = __uint_as_float(0x7FC00000u);
                 const float inv = 1.f / l[n][i];
                 if (!whole && g == 0) {

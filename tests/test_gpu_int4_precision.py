@@ -49,3 +49,52 @@ def test_query_entries_far_apart(D, bs, G, H, spread):
     kc[:, :, bs * D // 2:] = pair.repeat(bs)
     want, bound, _ = exact.decode(q, kc, vc, tables, lens, D ** -0.5, bs, weight=2.0 ** -11, centre=0.0)
     exact.check(_decode(q, kc, vc, tables, lens, D ** -0.5), want, bound, narrow=0.85)
+
+
+@pytest.mark.parametrize("D,bs,G,H", [(64, 8, 5, 3), (128, 16, 8, 2), (128, 32, 16, 1)])
+@pytest.mark.parametrize("offset", [0.0, 4.0])
+def test_codes_count_from_the_middle(D, bs, G, H, offset):
+    """A weight's rounding counts with a code's distance from 7.5, not with the code: elements whose codes lie in
+    the middle, and whose values are near zero, show it."""
+    q, kc, vc, tables, lens = _problem([2, 3, 4, 5, 6, 7, 9, 12, 33] * 3, G * H, H, D, bs, seed=D + G,
+                                       rows=lambda s, g: torch.randn(*s, generator=g) + offset)
+    q = q.to(torch.bfloat16)
+    want, bound, flat = exact.decode(q, kc, vc, tables, lens, D ** -0.5, bs)
+    exact.check(_decode(q, kc, vc, tables, lens, D ** -0.5), want, bound, flat)
+
+
+@pytest.mark.parametrize("qscale,scale", [(1.0, 3.0), (30.0, 0.088), (1.0, -0.7), (1e4, 0.088), (1e-3, 0.088)])
+@pytest.mark.parametrize("vscale", [1.0, 1e-30, 1e30])
+def test_sharp_and_flat_softmaxes(qscale, scale, vscale):
+    """Logits from a few units to thousands: the bound narrows with the softmax."""
+    D, bs, G, H = 128, 16, 4, 2
+    q, kc, vc, tables, lens = _problem([1, 40, 333, 700], G * H, H, D, bs, seed=17,
+                                       rows=lambda s, g: torch.randn(*s, generator=g) * vscale)
+    q = (q * qscale).to(torch.bfloat16)
+    want, bound, flat = exact.decode(q, kc, vc, tables, lens, scale, bs)
+    # a flat softmax is near the plain average: only the sharp ones can be told from it
+    exact.check(_decode(q, kc, vc, tables, lens, scale), want, bound, flat if qscale >= 1 else None, narrow=0.7)
+
+
+def test_long_runs_do_not_drift():
+    """220 stages of 32 tokens for every warp of the GPU.  The result rounded to bf16 differs from the 64-bit one's
+    rounding only where the weights' fp16 rounding, 2^-11 / sqrt(12) * 1.2 = 1.7e-4 relative in the mean square for
+    independent values, passes a border: sqrt(0.8 * 1.7e-4 * 2^-7.5) = 8.6e-4 in the mean square, half as much
+    again allowed.  (An accumulator that only truncates loses 2^-24 of itself twice a stage: a drift of 2.6e-5 of
+    the codes' sum, 2e-3 and more of these results, were it not kept near zero.)"""
+    B, H, D, bs, L, pool = 16, 8, 128, 16, 131072, 512
+    g = torch.Generator().manual_seed(5)
+    caches = []
+    for _ in range(2):
+        b, p = ref.pack_row(*ref.quantise(torch.randn(pool, H, bs, D, generator=g).to(torch.bfloat16)))
+        caches.append(torch.cat([b.flatten(2), p.flatten(2)], -1).contiguous())
+    q = (torch.randn(B, H, D, generator=g) * 0.5).to(torch.bfloat16)
+    tables = torch.stack([torch.cat([torch.randperm(pool, generator=g) for _ in range(L // bs // pool)])
+                          for _ in range(B)]).to(torch.int32)
+    got = _decode(q, *caches, tables, torch.full((B,), L, dtype=torch.int32), D ** -0.5)
+    # every block comes equally often: the softmax is that over the pool
+    k, v = (ref.values(c, bs, D).flatten(0, 1) for c in caches)
+    p = torch.softmax(torch.einsum("bhd,thd->bht", q.double(), k) * D ** -0.5, -1)
+    want = torch.einsum("bht,thd->bhd", p, v)
+    off = (got - want.to(torch.bfloat16).double()).norm() / want.norm()
+    assert float(off) <= 1.5 * 8.6e-4, float(off)
