@@ -91,7 +91,7 @@ struct Int4Cut {
     int64_t unit;         // where it starts in the weight (its part: [NG][chunk][lane] float4, at the kept place)
     int s, h, nt;
     int from, to;         // it began in an earlier worker / goes on in the next; both 0: no such part
-    float qa[8 * NG], m[8 * NG], l[8 * NG];
+    float m[8 * NG], l[8 * NG];  // maximum in units of log2, sum of the weights
 };
 
 __device__ __forceinline__ int int4_len(const Int4DecodeParams &p, int s, int block_size)
@@ -148,6 +148,13 @@ __device__ __forceinline__ void mma_codes(float *d, uint32_t a0, uint32_t a1, ui
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Larger magnitude of two pairs of fp16 values, a NaN giving way.
+__device__ __forceinline__ uint32_t max_abs_f16x2(uint32_t a, uint32_t b)
+{
+    const __half2 d = __hmax2(__habs2(*reinterpret_cast<__half2 *>(&a)), __habs2(*reinterpret_cast<__half2 *>(&b)));
+    return *reinterpret_cast<const uint32_t *>(&d);
 }
 
 // ev of vmul = 2^(10 - ev)
@@ -391,7 +398,8 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         // 2^-27 of the largest.  A word's operands lie together.  (A product of a subnormal code is cut 2^-25
         // below its nominal exponent: at 2^-15 of the largest entry of its 16 dims, for products of up to 15
         // times an entry.)
-        float qa[NG][2], qb[NG][2];
+        uint64_t qa[NG];  // a lane's two heads
+        float qb[NG][2];
         const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
@@ -433,13 +441,14 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             const float b = top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
                                            : sum * (sign * 9.765625e-4f) * pow2i(-(e >> 1)) * pow2i((e >> 1) - e);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                qa[n][i] = __shfl_sync(FULL, a, (2 * c + i) * 4);
-                qb[n][i] = __shfl_sync(FULL, b, (2 * c + i) * 4);
-            }
+            for (int i = 0; i < 2; ++i) qb[n][i] = __shfl_sync(FULL, b, (2 * c + i) * 4);
+            qa[n] = f32x2(__shfl_sync(FULL, a, 2 * c * 4), __shfl_sync(FULL, a, (2 * c + 1) * 4));
         }
 
-        float o[NG][MT][4], o1[NG][4], m[NG][2], mlim[NG][2], l[NG][2], zs[NG][2];  // m, mlim: in units of qa
+        // m: minus the running maximum, in units of log2; mlim: the logit / qa from which it moves; vmul =
+        // 2^(10 - ev): weights times value scales, in units of 2^m, were below 2^(ev + 1) when it was set
+        float o[NG][MT][4], o1[NG][4], m[NG][2], mlim[NG][2], vmul[NG][2], zs[NG][2];
+        uint64_t l[NG];
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
 #pragma unroll
@@ -448,16 +457,17 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m[n][i] = mlim[n][i] = -INFINITY;
-                o1[n][i] = o1[n][2 + i] = 0.f;
-                l[n][i] = zs[n][i] = 0.f;
+                m[n][i] = INFINITY;
+                mlim[n][i] = -INFINITY;
+                vmul[n][i] = pow2i(126);
+                o1[n][i] = o1[n][2 + i] = zs[n][i] = 0.f;
             }
+            l[n] = f32x2(0.f, 0.f);
         }
         // what the stages do not need waits in shared memory
         const int t1 = seg.t1, len = seg.len;
         int t = seg.t0;
         if (lane == 0) s_seg[warp] = seg;
-        float vmul = 0.f;     // 2^(10 - ev): the unit's value scales are below 2^(ev + 1) so far (0: none yet)
         unsigned poison = 0;
         __syncwarp();
 
@@ -523,46 +533,6 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                     }
             }
 
-            // ---- running maximum and value scale, moved only when a logit passes the
-            // maximum by more than 4 (so a weight stays below 2^4) or a scale its bound
-            const float vtop = fmaxf(fmaxf(fabsf(vp[0].x), fabsf(vp[1].x)), fmaxf(fabsf(vp[2].x), fabsf(vp[3].x)));
-            float top[NG][2];
-            bool move = vtop * vmul >= 2048.f;
-#pragma unroll
-            for (int n = 0; n < NG; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    top[n][i] = fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]), fmaxf(sc[1][n][i], sc[1][n][2 + i]));
-                    move |= top[n][i] > mlim[n][i];
-                }
-            if (__any_sync(FULL, move)) {
-                const int ve = (int)(__float_as_uint(vtop) >> 23) - 127;
-                const int ev = vmul == 0.f ? -1000 : int4_scale_exp(vmul);
-                const int en = max(max(ev, __reduce_max_sync(FULL, ve)), -100);
-                const float vcorr = exp2f((float)(ev - en));
-                vmul = pow2i(10 - en);
-#pragma unroll
-                for (int n = 0; n < NG; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float to = fmaxf(m[n][i], top[n][i]);
-#pragma unroll
-                        for (int off = 4; off <= 16; off <<= 1) to = fmaxf(to, __shfl_xor_sync(FULL, to, off));
-                        const float corr = m[n][i] == -INFINITY ? 0.f : exp2f(qa[n][i] * (m[n][i] - to));
-                        m[n][i] = to;
-                        mlim[n][i] = to + 4.f / qa[n][i];
-                        l[n][i] *= corr;  // a NaN stays one
-                        zs[n][i] *= corr;
-                        const float oc = corr * vcorr;
-                        o1[n][i] *= oc;
-#pragma unroll
-                        for (int k = 0; k < MT; ++k) {
-                            o[n][k][i] *= oc;
-                            o[n][k][2 + i] *= oc;
-                        }
-                    }
-            }
-
             // ---- weights: fp32 into l and the zeros' sum; times the value scale and rounded
             // to fp16 (2^-11 relative) for the tensor cores, one 8x8 transpose each.  Codes count from
             // 7.5: w c = w (c - 7.5) + 7.5 w, and what 7.5 times the rounded weights adds is taken out by
@@ -572,22 +542,89 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             // rounding.  The second tile takes 15 - c with negative weights: both its and the first
             // tile's accumulators stay near zero, where the tensor cores' truncation of long sums is small
             // (results of eight long sequences against the fp32 form's: 0.0025 off before, 0.0009 now).
-            uint32_t pf[NG][4];
+            //
+            // The maximum moves only when a logit passes it by more than 4, so a weight stays below 2^4.
+            // vmul, which brings a head's weights w = p s' into the fp16 range, is set where the maximum
+            // moves and where a scaled weight reaches 2^15, from the largest weight so far, not from the
+            // largest scale: a row far above the others counts only with its weight.  Both are rare: the
+            // stage's weights are made first and then, if they have to be, once more.
+            float top[NG][2];
+            bool move = false;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float vs = q < 2 ? vp[q].x * vmul : vp[q].x * -vmul, z = fmaf(7.5f, vp[q].x, vp[q].y);
+            for (int n = 0; n < NG; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    top[n][i] = fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]), fmaxf(sc[1][n][i], sc[1][n][2 + i]));
+                    move |= top[n][i] > mlim[n][i];
+                }
+            uint32_t pf[NG][4];
+            uint64_t ls[NG];
+            float zz[NG][2];
+            for (bool again = true;;) {
+                uint32_t big = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float vs = q < 2 ? vp[q].x : -vp[q].x, z = fmaf(7.5f, vp[q].x, vp[q].y);
+#pragma unroll
+                    for (int n = 0; n < NG; ++n) {
+                        const float *y = &sc[q >> 1][n][(q & 1) * 2];
+                        const float2 x = f32x2_split(fma_f32x2(qa[n], f32x2(y[0], y[1]), f32x2(m[n][0], m[n][1])));
+                        const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+                        const uint64_t pr = f32x2(p0, p1);
+                        ls[n] = q ? add_f32x2(ls[n], pr) : pr;
+                        zz[n][0] = q ? fmaf(p0, z, zz[n][0]) : p0 * z;
+                        zz[n][1] = q ? fmaf(p1, z, zz[n][1]) : p1 * z;
+                        const float2 w = f32x2_split(mul_f32x2(pr, f32x2(vs * vmul[n][0], vs * vmul[n][1])));
+                        pf[n][q] = pack_f16x2(w.x, w.y);
+                        big = max_abs_f16x2(big, pf[n][q]);
+                    }
+                }
+                move |= ((big + 0x08000800u) & 0x80008000u) != 0u;  // 2^15 or more, in either half
+                if (!__any_sync(FULL, move) || !again) break;
+                again = false;
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
-                    float w[2];
+                    const float2 qf = f32x2_split(qa[n]);
+                    float corr[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float pr = fast_exp2(qa[n][i] * (sc[q >> 1][n][(q & 1) * 2 + i] - m[n][i]));
-                        l[n][i] += pr;
-                        zs[n][i] = fmaf(pr, z, zs[n][i]);
-                        w[i] = pr * vs;
+                        const float a = i ? qf.y : qf.x;
+                        float to = top[n][i], wtop = 0.f;
+#pragma unroll
+                        for (int off = 4; off <= 16; off <<= 1) to = fmaxf(to, __shfl_xor_sync(FULL, to, off));
+                        const float mn = fminf(m[n][i], -(a * to));
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            wtop = fmaxf(wtop, fast_exp2(fmaf(a, sc[q >> 1][n][(q & 1) * 2 + i], mn)) * fabsf(vp[q].x));
+#pragma unroll
+                        for (int off = 4; off <= 16; off <<= 1) wtop = fmaxf(wtop, __shfl_xor_sync(FULL, wtop, off));
+                        // what was summed so far falls by 2^-by; it and this stage set the new power of two
+                        const float by = m[n][i] == INFINITY ? 400.f : fminf(m[n][i] - mn, 400.f);
+                        const int ev = int4_scale_exp(vmul[n][i]);
+                        const int en = min(max(max((int)(__float_as_uint(wtop) >> 23) - 127, ev - (int)by), -116), 127);
+                        m[n][i] = mn;
+                        mlim[n][i] = (4.f - mn) / a;
+                        vmul[n][i] = pow2i(10 - en);
+                        corr[i] = exp2f(-by);
+                        zs[n][i] *= corr[i];  // a NaN stays one
+                        const float oc = exp2f((float)(ev - en) - by);
+                        o1[n][i] *= oc;
+#pragma unroll
+                        for (int k = 0; k < MT; ++k) {
+                            o[n][k][i] *= oc;
+                            o[n][k][2 + i] *= oc;
+                        }
                     }
-                    pf[n][q] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+                    l[n] = mul_f32x2(l[n], f32x2(corr[0], corr[1]));
                 }
+            }
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                l[n] = add_f32x2(l[n], ls[n]);
+                const float2 z = f32x2_split(add_f32x2(f32x2(zs[n][0], zs[n][1]), f32x2(zz[n][0], zz[n][1])));
+                zs[n][0] = z.x, zs[n][1] = z.y;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) pf[n][q] = movmatrix_trans(pf[n][q]);
             }
 
             // ---- O += codes' . w: 16 dims x 8 heads x 16 tokens a step
@@ -653,32 +690,33 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 cut.to = was.t1 < was.nt;
             }
         }
-        const float f = pow2i(int4_scale_exp(vmul));  // out of the accumulators: 2^24 2^(ev - 10)
 #pragma unroll
         for (int n = 0; n < NG; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int hd = n * 8 + 2 * c + i;
+                const float2 lf = f32x2_split(l[n]);
+                float lt = i ? lf.y : lf.x, zt = zs[n][i];
 #pragma unroll
                 for (int off = 4; off <= 16; off <<= 1) {
-                    l[n][i] += __shfl_xor_sync(FULL, l[n][i], off);
-                    zs[n][i] += __shfl_xor_sync(FULL, zs[n][i], off);
+                    lt += __shfl_xor_sync(FULL, lt, off);
+                    zt += __shfl_xor_sync(FULL, zt, off);
                 }
-                zs[n][i] = fmaf(o1[n][i] * -7.5f, f, zs[n][i]);
-                if (poison) l[n][i] = __uint_as_float(0x7FC00000u);
-                const float inv = 1.f / l[n][i];
+                const float f = pow2i(int4_scale_exp(vmul[n][i]));  // out of the accumulators: 2^24 2^(ev - 10)
+                zt = fmaf(o1[n][i] * -7.5f, f, zt);
+                if (poison) lt = __uint_as_float(0x7FC00000u);
+                const float inv = 1.f / lt;
                 if (!whole && g == 0) {
-                    cut.qa[hd] = qa[n][i];
-                    cut.m[hd] = m[n][i];
-                    cut.l[hd] = l[n][i];
-                    if (part && hd < p.group) p.part_ml[2 * blockIdx.x * 16 + hd] = make_float2(m[n][i], l[n][i]);
+                    cut.m[hd] = -m[n][i];
+                    cut.l[hd] = lt;
+                    if (part && hd < p.group) p.part_ml[2 * blockIdx.x * 16 + hd] = make_float2(-m[n][i], lt);
                 }
 #pragma unroll
                 for (int k = 0; k < MT / 2; ++k) {  // dims 32 k + 4 g ..
                     const float4 r = make_float4(
-                        fmaf(o[n][2 * k][i] * 16384.f, f, zs[n][i]), fmaf(o[n][2 * k][2 + i] * 1024.f, f, zs[n][i]),
-                        fmaf(o[n][2 * k + 1][i] * 16384.f, f, zs[n][i]),
-                        fmaf(o[n][2 * k + 1][2 + i] * 1024.f, f, zs[n][i]));
+                        fmaf(o[n][2 * k][i] * 16384.f, f, zt), fmaf(o[n][2 * k][2 + i] * 1024.f, f, zt),
+                        fmaf(o[n][2 * k + 1][i] * 16384.f, f, zt),
+                        fmaf(o[n][2 * k + 1][2 + i] * 1024.f, f, zt));
                     const int cell = (n * Lay::kChunks + i * (MT / 2) + k) * 32 + lane;
                     if (hd >= p.group) continue;
                     if (whole)
@@ -714,7 +752,6 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
     };
     if (tid < 2 * W * H && ((parts >> (tid / H)) & 1u)) {
         const int e = tid / H, hd = tid % H;
-        const float fq = s_cut[e >> 1][e & 1].qa[hd];
         const unsigned run = run_of(e);
         float M = -INFINITY, L = 0.f;
         for (unsigned b = run; b; b &= b - 1) {
@@ -724,7 +761,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
         for (unsigned b = run; b; b &= b - 1) {
             const int x = __ffs(b) - 1;
             const Int4Cut<NG> &u = s_cut[x >> 1][x & 1];
-            const float f = fast_exp2(fq * (u.m[hd] - M));
+            const float f = fast_exp2(u.m[hd] - M);
             L = fmaf(f, u.l[hd], L);
             if (x == e) wf[tid] = f;
         }
@@ -835,18 +872,17 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             for (int i = 0; i < ITS; ++i) {
                 const int it = it0 + i * W * 32;
                 if (it >= items) break;
-                const float fq = u->qa[it / (D / 4)];
                 float to = M[i];
 #pragma unroll
                 for (int u = 0; u < U; ++u) to = fmaxf(to, ml[i][u].x);
-                const float corr = M[i] == -INFINITY ? 0.f : fast_exp2(fq * (M[i] - to));
+                const float corr = M[i] == -INFINITY ? 0.f : fast_exp2(M[i] - to);
                 float4 &acc = sums[i];
                 M[i] = to;
                 L[i] *= corr;
                 acc.x *= corr, acc.y *= corr, acc.z *= corr, acc.w *= corr;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const float f = fast_exp2(fq * (ml[i][u].x - to));
+                    const float f = fast_exp2(ml[i][u].x - to);
                     L[i] = fmaf(f, ml[i][u].y, L[i]);
                     acc.x = fmaf(f, r[i][u].x, acc.x);
                     acc.y = fmaf(f, r[i][u].y, acc.y);
@@ -875,7 +911,6 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
             __syncthreads();
             if (tid < items) {
                 const int hd = tid / (D / 4);
-                const float fq = u->qa[hd];
                 const float2 *ml = reinterpret_cast<const float2 *>(join + W * 32 * 16);
                 float M = -INFINITY, L = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -883,7 +918,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                 for (int y = 0; y < ways; ++y) {
                     const float2 v = ml[y * p.group + hd];
                     const float4 r = *reinterpret_cast<const float4 *>(join + (y * items + tid) * 16);
-                    const float f = fast_exp2(fq * (v.x - M));
+                    const float f = fast_exp2(v.x - M);
                     L = fmaf(f, v.y, L);
                     acc.x = fmaf(f, r.x, acc.x);
                     acc.y = fmaf(f, r.y, acc.y);

@@ -98,3 +98,40 @@ def test_long_runs_do_not_drift():
     want = torch.einsum("bht,thd->bhd", p, v)
     off = (got - want.to(torch.bfloat16).double()).norm() / want.norm()
     assert float(off) <= 1.5 * 8.6e-4, float(off)
+
+
+@pytest.mark.parametrize("ratio", [20, 26, 34, 60, 100])
+@pytest.mark.parametrize("at", ["first", "middle", "last"])
+@pytest.mark.parametrize("D,bs,G,H", [(128, 16, 8, 2), (64, 8, 12, 1)])
+def test_value_row_far_above_the_others(D, bs, G, H, ratio, at):
+    """A value row 2^ratio times the others, in sequences of one stage and of many.  It counts fully for a head that
+    attends to it, and not at all for one whose weight for it is far below 2^-ratio."""
+    lens = [20, 70, 700, 3000]
+    q, kc, vc, tables, ln = _problem(lens, G * H, H, D, bs, seed=ratio)
+    codes, pair = ref.quantise((torch.randn(len(lens), H, D, generator=torch.Generator().manual_seed(1))
+                                * 2.0 ** ratio).to(torch.bfloat16))
+    vb, vp = ref.pack_row(codes, pair)
+    kb, kp = ref.pack_row(*ref.quantise(torch.full((H, D), 3.0).to(torch.bfloat16)))
+    for i, n in enumerate(lens):
+        t = {"first": 0, "middle": n // 2, "last": n - 1}[at]
+        blk, o = int(tables[i, t // bs]), t % bs
+        for cache, b, p in ((vc, vb[i], vp[i]), (kc, kb, kp)):
+            cache[blk, :, o * D // 2:(o + 1) * D // 2] = b
+            cache[blk, :, bs * D // 2 + 4 * o:bs * D // 2 + 4 * o + 4] = p
+    # that row's key is 3 throughout: its logit is 3 scale sum q, far above or far below the others'
+    q = q - q.mean(-1, keepdim=True)
+    turn = torch.tensor([1.0 if h % 3 else -1.0 for h in range(G * H)])
+    q = (q + turn[None, :, None] * 160.0 / (3.0 * D * D ** -0.5)).to(torch.bfloat16)
+    want, bound, flat = exact.decode(q, kc, vc, tables, ln, D ** -0.5, bs)
+    got = _decode(q, kc, vc, tables, ln, D ** -0.5)
+    exact.check(got, want, bound)
+
+
+def test_value_scales_at_random():
+    """Value rows of all magnitudes from 2^-40 to 2^40, with logits that are as wide."""
+    D, bs, G, H = 128, 16, 4, 3
+    q, kc, vc, tables, lens = _problem([17, 90, 400, 900], G * H, H, D, bs, seed=3, rows=lambda s, g: torch.randn(
+        *s, generator=g) * torch.exp2(torch.randint(-40, 41, (*s[:3], 1), generator=g).float()))
+    q = (q * 12).to(torch.bfloat16)
+    want, bound, _ = exact.decode(q, kc, vc, tables, lens, D ** -0.5, bs)
+    exact.check(_decode(q, kc, vc, tables, lens, D ** -0.5), want, bound)
