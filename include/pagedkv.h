@@ -32,14 +32,17 @@
  *   the cudaError_t).  The library never aborts the process and never traps on
  *   the device.
  * - Every kernel is launched with programmatic dependent launch and, with the
- *   exceptions below, lets the next kernel of the stream start early.  The decode kernels read seq_lens,
- *   block_tables and query, and the pa_append_decode_kv* kernels seq_lens,
- *   block_tables, cow_src and the new key / value rows, before waiting for the
- *   previous kernel of the stream to finish (everything else after it); the
- *   kernels of this library that write those (pa_qk_norm_rope*, pa_prepare_batch,
- *   pa_release_blocks) never let the next kernel start early, and a kernel
+ *   exceptions below, lets the next kernel of the stream start early.  The decode
+ *   kernels read seq_lens, block_tables and query, and the pa_append_decode_kv*
+ *   kernels seq_lens, block_tables, cow_src and the new key / value rows, before
+ *   waiting for the previous kernel of the stream to finish (everything else after
+ *   it); the kernels of this library that write arrays which serve as those
+ *   (pa_qk_norm_rope*, pa_prepare_batch, pa_release_blocks, pa_decode_int4,
+ *   pa_dequantize_blocks_int4) never let the next kernel start early, and a kernel
  *   launched without that attribute (or one that never triggers its dependents
- *   early) is waited for as usual.
+ *   early) is waited for as usual.  The other decode calls and pa_prefill do let it
+ *   start early: their out must not be the query, key or value of a later call with
+ *   only kernels of this library between the two.
  * - Preconditions NOT checked in the launch path (pa_validate_tables checks
  *   them on the device): table entries below num_blocks for the blocks a
  *   sequence uses; ceil(seq_len/block_size) <= max_blocks_per_seq;

@@ -116,9 +116,10 @@ __global__ void append_kv_kernel(const uint4 *__restrict__ key, const uint4 *__r
                                  int64_t *__restrict__ slots_out, int num_seqs, int max_blocks,
                                  int chunks_per_token, int block_size, int64_t num_slots, float k_inv, float v_inv)
 {
-    // The lengths, the table and the new rows are inputs no kernel of this
-    // library writes: they are read before waiting for the previous kernel of
-    // the stream; the slot output and the cache are written after it.
+    // The lengths, the table and the new rows are read before waiting for the
+    // previous kernel of the stream: the kernels of this library that write such
+    // arrays let none after them start early.  The slot output and the cache are
+    // written after the wait.
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const bool live = i < (int64_t)num_seqs * chunks_per_token;
     int s = 0, c = 0;
@@ -179,9 +180,10 @@ __global__ void __launch_bounds__(256) append_kv_cow_kernel(
     const int32_t *__restrict__ cow_src, int64_t *__restrict__ slots_out, int max_blocks, int chunks_per_token,
     int block_size, int rows_per_cta, int64_t num_blocks)
 {
-    // The lengths, the table and the copy sources are inputs no kernel of this
-    // library writes: they are read before waiting for the previous kernel of
-    // the stream; the caches and the slot output are touched after it.
+    // The lengths, the table and the copy sources are read before waiting for the
+    // previous kernel of the stream: the kernels of this library that write such
+    // arrays let none after them start early.  The caches and the slot output are
+    // touched after the wait.
     const int s = blockIdx.y;
     const int r0 = blockIdx.x * rows_per_cta;
     const int r1 = min(block_size, r0 + rows_per_cta);

@@ -333,8 +333,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     }
     // Programmatic dependent launch: this grid may start while the previous
     // kernel of the stream still runs.  The enumeration below reads only the
-    // lengths (and the scheduler the tables and queries), which no kernel of
-    // this library writes, so it runs before griddepcontrol.wait; every
+    // lengths (and the scheduler the tables and queries); the kernels of this
+    // library that write such arrays let none after them start early (the
+    // exceptions, out of pa_decode* and pa_prefill as a query, the header rules
+    // out), so it runs before griddepcontrol.wait; every
     // access to the caches, the outputs, the workspace and its counters comes
     // after it (producer before its first load, scheduler before its first
     // counter access, all threads before the partitions-only fill and the

@@ -380,8 +380,9 @@ __global__ void __launch_bounds__(256)
     const int lane = threadIdx.x & 31;
     const int gl = lane % LPR, grp = lane / LPR;
     const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    // It writes rows that the append kernels after it may read before their own
+    // griddepcontrol.wait: it never lets them start early.
     pdl_wait();
-    pdl_launch_dependents();
     if (unit >= units) return;
     const int64_t i = unit / (2 * num_kv_heads);
     const int r = (int)(unit - i * 2 * num_kv_heads);

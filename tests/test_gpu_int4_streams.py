@@ -1,5 +1,6 @@
-"""GPU: default outputs of the 4-bit cache and rotation calls on a stream that is
-not the current one: the current stream's late work must not land on them."""
+"""GPU: what lies between two calls of the 4-bit cache.  Default outputs on a stream
+that is not the current one: the current stream's late work must not land on them.
+Results that the next call of the stream reads ahead of its own wait."""
 
 import pytest
 import torch
@@ -69,3 +70,44 @@ def test_results_on_another_stream(form):
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g, w) and bool(w.any())
+
+
+def test_read_back_rows_appended_at_once():
+    """Rows of the read-back as the new rows of the next call, which reads them ahead of its own wait."""
+    nb, bs, H, D = 2000, 16, 8, 128
+    kc, vc = _caches(nb, bs, H, D)
+    ids = torch.randperm(nb, generator=torch.Generator().manual_seed(3)).to(torch.int32).to(DEV)
+    B = nb * bs
+    tables = torch.arange(nb, dtype=torch.int32, device=DEV).repeat_interleave(bs)[:, None].contiguous()
+    lens = (torch.arange(B, device=DEV) % bs + 1).to(torch.int32)
+    ko, vo = (torch.zeros(nb, bs, H, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    a, b = torch.zeros_like(ko), torch.zeros_like(vo)
+    for shift in range(4):
+        order = ids.roll(shift)
+        ops.dequantize_blocks_int4(kc, vc, order, D, key_out=ko, value_out=vo)
+        ops.append_decode_kv(ko.view(B, H, D), vo.view(B, H, D), a, b, tables, lens)
+        torch.cuda.synchronize()
+        assert torch.equal(a, ko) and torch.equal(b, vo)
+
+
+def test_result_as_the_next_query():
+    """The 4-bit decode's result as the query of a bf16 decode right after it."""
+    nb, bs, H, D, B, Hq = 600, 16, 2, 128, 6, 16
+    kc, vc = _caches(nb, bs, H, D)
+    kb, vb = ops.dequantize_blocks_int4(kc, vc, torch.arange(nb, dtype=torch.int32, device=DEV), D)
+    tables = torch.randperm(nb, generator=torch.Generator().manual_seed(4)).to(torch.int32).to(DEV).view(B, -1).contiguous()
+    lens = torch.tensor([1600, 3, 900, 1599, 64, 1000], dtype=torch.int32, device=DEV)
+    ws, ws2 = ops.new_int4_workspace(Hq, H, D), ops.new_workspace(B, Hq, H, D, 1600)
+    q = _rows(B, Hq, D, seed=9)
+    mid, out = torch.zeros_like(q), torch.zeros_like(q)
+
+    def second(query):
+        return ops.decode(query, kb, vb, tables, lens, 0.3, 1600, workspace=ws2, out=out)
+
+    want = second(ops.decode_int4(q, kc, vc, tables, lens, 0.3, ws).clone()).clone()
+    for _ in range(20):
+        mid.zero_()
+        ops.decode_int4(q, kc, vc, tables, lens, 0.3, ws, out=mid)
+        second(mid)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
