@@ -500,7 +500,8 @@ int pa_qk_norm_rope_cache_int4(void *query_out, const void *query, const void *k
  * With one of the first two errors nothing is handed out: the tables stay as
  * they are, seq_lens are the context lengths (clamped to the row), q_start is 0
  * and every row -1.  seq_ids, positions and slot_mapping may be NULL; seq_lens
- * may be context_lens itself.
+ * may be context_lens or query_lens itself (another overlap of seq_lens or q_start
+ * with those is PA_ERR_BAD_SHAPE at the call).
  * The seq_lens and tables written here may be read by later kernels before they
  * wait: these kernels never let the next kernel start early.
  *

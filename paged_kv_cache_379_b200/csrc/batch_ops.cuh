@@ -113,8 +113,8 @@ __device__ __forceinline__ void fill_token(const BatchParams &p, int t)
         return;
     }
     const int s = request_of([&](int i) { return p.q_start[i]; }, p.num_seqs, t);
-    // positions stay below max_blocks * block_size, which fits 31 bits
-    const int64_t pos = (int64_t)p.seq_lens[s] - p.query_lens[s] + (t - p.q_start[s]);
+    // positions stay below max_blocks * block_size, which fits 31 bits; query_lens may be overwritten by now
+    const int64_t pos = (int64_t)p.seq_lens[s] - p.q_start[s + 1] + t;
     write_token(p, t, s, pos, p.block_tables[(int64_t)s * p.max_blocks + div_block(p, (uint32_t)pos)]);
 }
 

@@ -1336,6 +1336,15 @@ int pa_prepare_batch(int32_t *block_tables, const int32_t *context_lens, const i
     if (!num_free || !num_free_out || !status || !q_start) return PA_ERR_NULL_POINTER;
     if (num_seqs > 0 && (!block_tables || !context_lens || !query_lens || !seq_lens)) return PA_ERR_NULL_POINTER;
     if (free_capacity > 0 && !free_blocks) return PA_ERR_NULL_POINTER;
+    // lengths are updated in place or apart: a shifted overlap would be read after it was written
+    auto apart = [](const int32_t *a, int64_t n, const int32_t *b, int64_t m) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+        return x + n * sizeof(int32_t) <= y || y + m * sizeof(int32_t) <= x;
+    };
+    for (const int32_t *in : {context_lens, query_lens}) {
+        if (seq_lens != in && !apart(seq_lens, num_seqs, in, num_seqs)) return PA_ERR_BAD_SHAPE;
+        if (num_seqs > 0 && !apart(q_start, (int64_t)num_seqs + 1, in, num_seqs)) return PA_ERR_BAD_SHAPE;
+    }
     BatchParams p = {};
     p.block_tables = block_tables;
     p.context_lens = context_lens;
@@ -1358,9 +1367,8 @@ int pa_prepare_batch(int32_t *block_tables, const int32_t *context_lens, const i
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     divisor(block_size, p.div_mul, p.div_shift);
     // several CTAs where no output is an input, and a request's sums fit each one's copy
-    auto apart = [](const int32_t *a, const int32_t *b, int n) { return a + n <= b || b + n <= a; };
-    const bool alone = !apart(seq_lens, context_lens, num_seqs) || !apart(seq_lens, query_lens, num_seqs) ||
-                       num_free_out == num_free || num_seqs > kBatchSmemSeqs;
+    const bool alone = seq_lens == context_lens || seq_lens == query_lens || num_free_out == num_free ||
+                       num_seqs > kBatchSmemSeqs;
     const bool fused = !alone || num_tokens <= kBatchFusedTokens;
     const unsigned ctas = alone ? 1u : std::max(1u, (unsigned)cdiv64(num_tokens, kBatchRows));
     const int rc = launch_pdl(prepare_batch_kernel, dim3(ctas), dim3(kBatchThreads), 0, st, p, fused ? 1 : 0);

@@ -1,8 +1,11 @@
-"""The 4-bit cache's binding on a host without CUDA."""
+"""The 4-bit cache's and the batch preparation's calls on a host without a GPU."""
 
+import ctypes
 import os
 import subprocess
 import sys
+
+from paged_kv_cache_379_b200 import _lib
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -25,3 +28,17 @@ else:
 """
     done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert done.returncode == 0, done.stderr
+
+
+def test_prepare_batch_refuses_shifted_overlaps():
+    P = ctypes.c_void_p
+    at = dict(bt=0x10000, ctx=0x20000, new=0x30000, free=0x40000, nf=0x50000, sl=0x60000, qs=0x70000, ids=None, pos=None,
+              slots=None, nfo=0x80000, status=0x90000)
+
+    def call(**kw):
+        ptrs = [v and P(v) for v in dict(at, **kw).values()]
+        return _lib.load().pa_prepare_batch(*ptrs, 4, 8, 16, 100, 16, 100, None)
+
+    for kw in (dict(sl=0x20004), dict(sl=0x1FFFC), dict(sl=0x3000C), dict(sl=0x2FFF4), dict(qs=0x20000), dict(qs=0x2FFF0),
+               dict(qs=0x3000C)):
+        assert call(**kw) == -2, kw
