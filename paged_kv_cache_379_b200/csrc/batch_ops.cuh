@@ -209,9 +209,11 @@ __global__ void __launch_bounds__(kBatchThreads) prepare_batch_kernel(const Batc
     }
     if (!fused) return;
     __syncthreads();
-    const int t0 = blockIdx.x * kBatchRows;
-    const int t1 = gridDim.x > 1 ? min(p.num_tokens, t0 + kBatchRows) : p.num_tokens;
-    for (int t = t0 + tid; t < t1; t += kBatchThreads) {
+    // 64 bits: the step past the last rows may pass 31
+    const int64_t t0 = (int64_t)blockIdx.x * kBatchRows;
+    const int t1 = gridDim.x > 1 ? (int)min((int64_t)p.num_tokens, t0 + kBatchRows) : p.num_tokens;
+    for (int64_t row = t0 + tid; row < t1; row += kBatchThreads) {
+        const int t = (int)row;
         if (!near) {  // one CTA: all of it is its own
             fill_token(p, t);
         } else if (t >= (int)carry_tok) {
