@@ -374,6 +374,9 @@ int pa_decode_fp8_split(void *out, const void *query, const void *key_cache,
  * every step one fp32 operation rounded to nearest even.  Where the scale would
  * be below 2^-126 it is 0 and so are the codes.  A row that holds a NaN or an
  * infinity stands for NaN throughout (zero = NaN, scale = 0, codes 0).
+ * The calls that read a cache take any finite scale and zero, a negative scale too.
+ * Whole blocks are contiguous: pa_copy_blocks and pa_swap_blocks move them as those
+ * of a bf16 cache of block_size 1 and head_dim record / 2.
  * Supported: head_dim 64 or 128, block_size 8, 16 or 32.
  *
  * pa_reshape_and_cache_int4: pa_reshape_and_cache with quantisation.  key and
@@ -405,7 +408,9 @@ int pa_dequantize_blocks_int4(void *key_out, void *value_out, const void *key_ca
  * and V the values the codes stand for (G = num_heads / num_kv_heads in 1..16;
  * scale finite).
  * The work is split over the GPU by the lengths found on the device, so no
- * bound of the lengths is passed; one launch.  A length of 0 or less gives
+ * bound of the lengths is passed; one launch.  The query enters exactly, logits and
+ * sums are fp32; the weights of the values are rounded to fp16 (2^-11 relative), which
+ * counts with a code's distance from the middle, 7.5.  A length of 0 or less gives
  * zeros, a length past max_blocks_per_seq * block_size counts as that.  A table
  * entry outside [0, num_blocks) among the blocks of a sequence is not followed:
  * the sequence's outputs are NaN for the KV heads concerned (all of them) and

@@ -15,7 +15,8 @@ Tensor conventions (see include/pagedkv.h):
   FP8 caches             : uint8 E4M3 codes [num_blocks, block_size, num_kv_heads, head_dim]
                            with one fp32 scale per cache (k_scale, v_scale)
   4-bit caches             : uint8 [num_blocks, num_kv_heads, block_size * (head_dim / 2 + 4)]
-                           (codes, then a bf16 (scale, zero) pair per row; new_int4_cache)
+                           (codes, then a bf16 (scale, zero) pair per row; new_int4_cache);
+                           copy_blocks and swap_blocks take cache.view(torch.bfloat16).unsqueeze(1)
 """
 
 from __future__ import annotations
