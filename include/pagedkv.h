@@ -408,8 +408,10 @@ int pa_dequantize_blocks_int4(void *key_out, void *value_out, const void *key_ca
  * and V the values the codes stand for (G = num_heads / num_kv_heads in 1..16;
  * scale finite).
  * The work is split over the GPU by the lengths found on the device, so no
- * bound of the lengths is passed; one launch.  The query enters exactly, logits and
- * sums are fp32; the weights of the values are rounded to fp16 (2^-11 relative), which
+ * bound of the lengths is passed; one launch.  Logits and sums are fp32.
+ * In fewer bits: the query in fp16, scaled by each head's largest entry (exact down to
+ * 2^-27 of it; the tensor cores cut 16 products with codes at a time at 2^-15 of the
+ * largest entry among them), and the weights of the values (2^-11 relative), which
  * counts with a code's distance from the middle, 7.5.  A length of 0 or less gives
  * zeros, a length past max_blocks_per_seq * block_size counts as that.  A table
  * entry outside [0, num_blocks) among the blocks of a sequence is not followed:

@@ -576,7 +576,8 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                         ls[n] = q ? add_f32x2(ls[n], pr) : pr;
                         zz[n][0] = q ? fmaf(p0, z, zz[n][0]) : p0 * z;
                         zz[n][1] = q ? fmaf(p1, z, zz[n][1]) : p1 * z;
-                        const float2 w = f32x2_split(mul_f32x2(pr, f32x2(vs * vmul[n][0], vs * vmul[n][1])));
+                        // p s' first: it is finite, and 0 where p is, whatever vmul still is
+                        const float2 w = f32x2_split(mul_f32x2(mul_f32x2(pr, f32x2(vs, vs)), f32x2(vmul[n][0], vmul[n][1])));
                         pf[n][q] = pack_f16x2(w.x, w.y);
                         big = max_abs_f16x2(big, pf[n][q]);
                     }

@@ -135,3 +135,22 @@ def test_value_scales_at_random():
     q = (q * 12).to(torch.bfloat16)
     want, bound, _ = exact.decode(q, kc, vc, tables, lens, D ** -0.5, bs)
     exact.check(_decode(q, kc, vc, tables, lens, D ** -0.5), want, bound)
+
+
+def test_scaled_row_of_no_weight_after_constant_rows():
+    """Value rows of scale 0 set no range; a row of a large scale whose weight is 0 must leave the result alone."""
+    D, bs, G, H, L = 128, 16, 4, 1, 200
+    q, kc, vc, tables, lens = _problem([L, 40], G * H, H, D, bs, seed=2,
+                                       rows=lambda s, g: torch.randn(*s[:3], 1, generator=g).expand(*s))
+    vb, vp = ref.pack_row(*ref.quantise((torch.randn(1, D, generator=torch.Generator().manual_seed(1)) * 64).to(torch.bfloat16)))
+    kb, kp = ref.pack_row(*ref.quantise(torch.full((1, D), 3.0).to(torch.bfloat16)))
+    for i, t in ((0, 100), (0, 199), (1, 3)):
+        blk, o = int(tables[i, t // bs]), t % bs
+        for cache, b, p in ((vc, vb, vp), (kc, kb, kp)):
+            cache[blk, :, o * D // 2:(o + 1) * D // 2] = b
+            cache[blk, :, bs * D // 2 + 4 * o:bs * D // 2 + 4 * o + 4] = p
+    q = q - q.mean(-1, keepdim=True)
+    turn = torch.tensor([-1.0, 1.0, -1.0, -1.0])
+    q = (q + turn[None, :, None] * 160.0 / (3.0 * D * D ** -0.5)).to(torch.bfloat16)
+    want, bound, _ = exact.decode(q, kc, vc, tables, lens, D ** -0.5, bs)
+    exact.check(_decode(q, kc, vc, tables, lens, D ** -0.5), want, bound)
