@@ -440,9 +440,12 @@ static int check_int4_cache(const void *key_cache, const void *value_cache, int 
     return PA_OK;
 }
 
-// Groups of rows from which on a warp takes 8 of them: 16384 tokens of 48 rows (393 K
-// groups) take 75.9 us with 8, 84.6 with 2; 128 tokens of 80 rows (5 K) 4.8 and 3.6 us.
-static constexpr int64_t kRowsWide = 148 * 64 * 8;
+// Groups of rows from which on a warp takes 8 of them.  2 against 8, in us: half-split pairs,
+// bf16 cache, head_dim 128, 10 K groups 4.45 and 5.17, 14 K 5.37 and 5.33, 40 K 12.3 and 10.9,
+// 150 K 45.3 and 37.2; interleaved pairs 10 K 3.52 and 4.72, 30 K 7.19 and 7.24.  A 4-bit
+// cache takes 2 always: 393 K groups, head_dim 128, 127 and 139 us (interleaved 99.8 and
+// 97.5), head_dim 64 64 and 79 (52 and 55).
+static constexpr int64_t kRowsWide = 148 * 32 * 8;
 
 template <int D, int CACHE, int U>
 static int launch_rows_u(RowParams &p, int num_tokens, bool interleaved, cudaStream_t st)
@@ -461,10 +464,12 @@ static int launch_rows_u(RowParams &p, int num_tokens, bool interleaved, cudaStr
 template <int CACHE>
 static int launch_rows(RowParams &p, int head_dim, int num_tokens, bool interleaved, cudaStream_t st)
 {
-    const int64_t groups = (int64_t)num_tokens * cdiv64(p.rows, 32 / (head_dim / 8));
-    if (groups >= kRowsWide)
-        return head_dim == 64 ? launch_rows_u<64, CACHE, 8>(p, num_tokens, interleaved, st)
-                              : launch_rows_u<128, CACHE, 8>(p, num_tokens, interleaved, st);
+    if constexpr (CACHE != kCacheInt4) {
+        const int64_t groups = (int64_t)num_tokens * cdiv64(p.rows, 32 / (head_dim / 8));
+        if (groups >= kRowsWide)
+            return head_dim == 64 ? launch_rows_u<64, CACHE, 8>(p, num_tokens, interleaved, st)
+                                  : launch_rows_u<128, CACHE, 8>(p, num_tokens, interleaved, st);
+    }
     return head_dim == 64 ? launch_rows_u<64, CACHE, 2>(p, num_tokens, interleaved, st)
                           : launch_rows_u<128, CACHE, 2>(p, num_tokens, interleaved, st);
 }

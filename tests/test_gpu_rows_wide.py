@@ -1,5 +1,5 @@
-"""GPU: head norm + rotation where a warp takes 8 groups of rows (75776 groups and more), in every cache form, and a
-table of cosines past 2^31 bytes."""
+"""GPU: head norm + rotation of many tokens, where a warp takes 8 groups of rows instead of 2 (from 37888 groups on, but
+for the 4-bit cache), in every cache form, and a table of cosines past 2^31 bytes."""
 
 import pytest
 import torch
@@ -10,7 +10,7 @@ from test_gpu_rows import _close, _inputs, _table, _views
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-WIDE = 148 * 64 * 8  # groups of 32 / (D / 8) rows
+WIDE = 148 * 32 * 8  # groups of 32 / (D / 8) rows
 
 
 def _new(form, nb, bs, H, D):
