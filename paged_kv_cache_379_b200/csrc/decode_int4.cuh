@@ -15,20 +15,21 @@
 // Work: a unit is one sequence and KV head, a stage 32 of its tokens.  The weight of
 // all units is cut into equal ranges, one for each warp of the grid, so a long
 // sequence spreads over the GPU and short ones share a warp; a warp runs through its
-// range alone, with its own ring of stages (cp.async, 16 bytes a lane: the records'
-// bulk copies took 581 instead of 565 instructions a stage) and its own online
+// range alone, with its own ring of stages (cp.async, 16 bytes a lane: in an earlier form
+// of the stage 565 instructions, with the records' bulk copies 581) and its own online
 // softmax.  Units cut between warps are joined once, at the CTA's end, and between
 // CTAs by the last of them to arrive, in a fixed order.  (Ranges for CTAs, whose
 // warps take turns at a unit's stages and join at its end: 48.9 instead of 43.7 us
 // for the grouped-query batch, 8.7 instead of 3.8 for four short sequences.)
 //
 // Bound, head_dim 128 and block_size 16, one launch after another: eight sequences of
-// 32K-128K tokens (713 MB) 131 to 138 us from GPU to GPU, 80 to 83 % of the measured
-// copy rate, its stages near that rate and the rest the start (4 us) and the join; 128 sequences of ~1100 tokens, 8
-// query heads on each of 8 KV heads (160 MB) 42 us, 64 sequences with 32 heads (323
-// MB) 69 us: 26 and 51 us of stages, 4 of start, the rest the join, where the SMs
-// wait for their last warps and for cold code.  A stage takes about 440
-// instructions: 58 % of the issue slots, 49 % of the pipe of the ANDs.
+// 32K-128K tokens (713 MB) 141 to 151 us from GPU to GPU, 72 to 77 % of the measured
+// copy rate; 128 sequences of ~1100 tokens, 8 query heads on each of 8 KV heads (160 MB)
+// 46 us, 64 sequences with 32 heads (323 MB) 74 us; one of 8001 15.3, four of at most 50
+// 5.6.  A stage takes 465 instructions (set-up and join included), half of them on the
+// pipe of the ANDs: 55 % of the issue slots, 57 % of that pipe and 32 % of the tensor
+// cores' cycles in the long case.  An SM is active for 91 % of that launch and 85 % of the
+// grouped-query one; the rest is the spread of the last warps and the join.
 // Included once, by pagedkv.cu.
 #pragma once
 
@@ -77,7 +78,11 @@ struct Int4Lay {
 };
 
 // A unit (sequence, KV head) of nt stages weighs nt + kI4UnitCost stages when the
-// work is cut into ranges: what its queries' set-up and its result take.
+// work is cut into ranges: what its queries' set-up and its result take.  2, 4 and 6 take
+// 45.2, 45.9 and 47.4 us for the grouped-query batch, 72.1, 73.4 and 75.7 for 32 heads on
+// 32, but 17.3, 15.4 and 15.2 for one 8K sequence, 56.8, 54.1 and 54.8 for 64 sequences
+// with 16 heads a KV head and 58.3, 49.2 and 49.7 for four long ones with 12 (head_dim 64:
+// within 2 %).
 constexpr int kI4UnitCost = 4;
 
 // A run of stages [t0, t1) of one unit in a worker's range.

@@ -531,8 +531,9 @@ static Int4Workspace int4_workspace(int group, int head_dim)
 }
 
 // Fewest stages (32 tokens of one KV head) worth a warp of their own: 2, 4 and 8 take
-// 16.5, 17.2 and 17.2 us for one 8K sequence, 3.8, 5.2 and 7.3 for four short ones at a
-// unit cost of 2 stages; at a cost of 4, 4 stages take 13.6 and 3.8 us.
+// 17.6, 15.4 and 17.8 us for one 8K sequence (head_dim 64: 12.5, 12.0, 13.5; 12 heads a KV
+// head, 3K: 18.5, 17.7, 19.9) and 5.9, 5.8 and 8.4 for four short ones; batches of many
+// ranges are the same with all three.
 static constexpr int kI4MinStages = 4;
 
 template <int D, int BS, int NG>

@@ -9,7 +9,7 @@
 //   BS rows of D/2 code bytes (dim 2i in the low nibble of byte i, dim 2i+1 in
 //   the high one), then BS pairs (scale, zero) of bf16.  A code c of row o stands
 //   for zero_o + scale_o * c.  The record of one head of a block is contiguous
-//   (1088 bytes at D = 128, BS = 16), so the decode fetches it with one bulk copy.
+//   (1088 bytes at D = 128, BS = 16), so the decode's 16-byte copies cover whole lines.
 // A row is quantised against its own minimum and maximum:
 //   zero = min x (a bf16 value already), scale = bf16(fp32(max r) - fp32(min r)),
 //   r = fp32(1/15)  (the two products keep max - min from overflowing),
@@ -206,8 +206,10 @@ __global__ void __launch_bounds__(128) store_int4_kernel(const RowParams p)
 // them and every lane has U loads in flight.  Each row is read and written once:
 // 16384 tokens of 32 + 8 + 8 heads (407 MB) take 75 us, 83 % of the measured copy
 // rate; beside that bound, instructions (the norm's and the rotation's, ~150 for two
-// rows) take two thirds of the issue slots.  One step's 128 tokens: 3.3 us, launch
-// and latency.
+// rows) take two thirds of the issue slots.  Half-split pairs over the whole head, whose
+// partners come by shuffles, take 91 us (an FP8 cache as much); a 4-bit cache, quantised
+// with 8 values a lane, 99 us interleaved and 126 half-split.  One step's 128 tokens: 3.3
+// us (4-bit 3.8), launch and latency.
 template <int D, int CACHE, bool INTERLEAVED, int U>
 __global__ void __launch_bounds__(256) row_kernel(const RowParams p)
 {
