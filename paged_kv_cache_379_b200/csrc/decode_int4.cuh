@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kI4Warps * 32, Int4Lay<D, BS, NG>::kCtas)
                         y = fmaf(kp.x, y, kp.y * qb[n][i]);
                     }
             }
-            if ((t + 1) * kI4Tokens > len) {
+            if (len - t * kI4Tokens < kI4Tokens) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     if (t * kI4Tokens + q * 8 + g >= len) {
