@@ -408,7 +408,8 @@ int pa_dequantize_blocks_int4(void *key_out, void *value_out, const void *key_ca
  * and V the values the codes stand for (G = num_heads / num_kv_heads in 1..16;
  * scale finite).
  * The work is split over the GPU by the lengths found on the device, so no
- * bound of the lengths is passed; one launch.  Logits and sums are fp32.
+ * bound of the lengths is passed; one launch.  Logits and sums are fp32 (a head
+ * whose largest logit times log2 e passes its range comes out NaN).
  * In fewer bits: the query in fp16, scaled by each head's largest entry (exact down to
  * 2^-27 of it; the tensor cores cut 16 products with codes at a time at 2^-15 of the
  * largest entry among them), and the weights of the values (2^-11 relative), which

@@ -44,6 +44,19 @@ def test_read_back_on_another_stream(as_handle):
         assert torch.equal(g, w) and not bool(g[1].any()) and bool(g[0].any())
 
 
+def test_read_back_on_the_default_stream_by_handle():
+    """Handle 0 while another stream is current."""
+    kc, vc = _caches()
+    ids = torch.tensor([3, -1, 0, 5], dtype=torch.int32, device=DEV)
+    want = [t.clone() for t in ops.dequantize_blocks_int4(kc, vc, ids, 128)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda._sleep(SLEEP)
+        got = ops.dequantize_blocks_int4(kc, vc, ids, 128, stream=0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
 @pytest.mark.parametrize("form", ["decode", "rope", "rope_cache"])
 def test_results_on_another_stream(form):
     kc, vc = _caches()
